@@ -45,6 +45,7 @@
 #ifndef LITEATTN_H
 #define LITEATTN_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -347,6 +348,145 @@ int lite_attn_timing_read(lite_attn_plan_t plan, double *attn_ms, double *step_m
 #define LITE_NOALLOC_MAX_PAIRS 65536
 int lite_attn_compact_noalloc(const uint32_t *bits, int B, int H, int N, int Br, int Bc, uint32_t *list,
                               int32_t *cnt, int32_t *order, int64_t *live_total, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Serving attention: grouped query heads, packed sequences of different
+ * lengths, and a paged cache of keys and values.
+ *
+ * These calls have no counterpart in the pages.  They are what surrounds the
+ * step above in a pipeline that generates token by token or frame by frame:
+ * the prompt (or a whole token sequence) is read once with lite_attn_prompt,
+ * new tokens' keys and values enter a paged cache with lite_attn_cache_append
+ * (the position rotation applied on the way), and the new tokens attend over
+ * the cache with lite_attn_cache_attend, one token or a frame of them at a time.
+ *
+ * Shared by them, beside the conventions at the top of this file:
+ * - A grouped-query plan fixes Hq query heads, Hk key heads (query head h reads
+ *   key head h / (Hq / Hk)), d and the 16-bit type of all tensors.  It belongs
+ *   to the device that was current when it was created.  It holds no scratch:
+ *   calls with different workspaces may overlap on different streams.
+ * - Tensors are [tokens][heads][d] views (lite_attn_rows_t): d contiguous, token
+ *   and head strides multiples of 8 elements, 16-byte aligned, so slices of a
+ *   fused projection serve as they are.
+ * - Batches are ragged and live on the device: sequence b has the query tokens
+ *   [cu[b], cu[b + 1]) (int32, cu[0] <= ... <= cu[B]).  Token rows outside
+ *   [cu[0], cu[B]) are neither read for a result nor written, so padded
+ *   batches and captured graphs replayed on other lengths are fine.  The
+ *   queries are the LAST n of the sequence's m positions: query token t sees
+ *   the keys 0 .. m - n + t (causal) or all m.  A row that sees no key gets
+ *   zeros.  What stands in places that no row sees (NaN included) has no effect.
+ * - What the kernels find wrong in device data (lengths outside the tensors,
+ *   a page that does not exist, an angle row out of range) is not used as an
+ *   address: the sequence or token is left out and the plan's status becomes
+ *   LITE_ERR_DEVICE_CHECK (sticky; lite_attn_gqa_status).
+ * - Logits, softmax statistics and output sums are held in 32 bits; the
+ *   weights are rounded to the tensors' type for the product with the values
+ *   and the output is rounded once.  Results are the same on every run. */
+typedef struct lite_attn_gqa *lite_attn_gqa_t;
+
+#define LITE_DTYPE_BF16 0
+#define LITE_DTYPE_FP16 1
+
+/* A [tokens][heads][d] view; strides in elements. */
+typedef struct {
+    void *ptr;
+    int64_t tokens, stride_token, stride_head;
+} lite_attn_rows_t;
+
+/* Create a grouped-query plan: Hq % Hk == 0, d 64 or 128, Hq / Hk <= 128.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALLOC, CUDA. */
+int lite_attn_gqa_create(lite_attn_gqa_t *out, int Hq, int Hk, int d, int dtype);
+
+/* Free a plan (synchronises the device first).  NULL is accepted and ignored. */
+int lite_attn_gqa_destroy(lite_attn_gqa_t plan);
+
+/* The plan's status after the work on `stream` (which is synchronised):
+ * LITE_OK, LITE_ERR_DEVICE_CHECK or LITE_ERR_DEVICE_TIMEOUT (sticky). */
+int lite_attn_gqa_status(lite_attn_gqa_t plan, void *stream);
+
+/* Bytes of workspace that an attention call needs (0: none): B sequences,
+ * `tokens` query rows in the tensor, at most max_new query tokens and max_keys
+ * keys in a sequence (lite_attn_prompt: the tensors' tokens for both;
+ * lite_attn_cache_attend: its max_new and table_width * page). */
+int lite_attn_gqa_workspace(lite_attn_gqa_t plan, int B, int64_t tokens, int max_new, int64_t max_keys,
+                            size_t *bytes);
+
+/* New tokens into the cache.
+ *   k, v     : the new keys and values, `tokens` rows of Hk heads.
+ *   q, q_out : queries to rotate beside them, Hq heads (ptr NULL: none);
+ *              q_out == q rotates in place.
+ *   k_pages, v_pages : the cache, `pages` pages of `page` tokens (a power of
+ *              two from 16 to 65536), each [pages][Hk][page][d]
+ *              (LITE_LAYOUT_BHND) or [pages][page][Hk][d] (LITE_LAYOUT_BNHD).
+ *   cos, sin : device float [angle_rows][rot / 2], 16-byte aligned, or NULL
+ *              for no rotation.  With the row of a token,
+ *              (a, b) -> (a cos - b sin, a sin + b cos) for the pairs
+ *              (i, i + rot/2), or (2i, 2i + 1) with `interleaved`, of the first
+ *              `rot` elements (a multiple of 16) of every head of q and k,
+ *              in 32 bits, rounded once.  One angle per position and pair covers
+ *              any axes: rows are whatever the caller's table holds.
+ *   positions: device [tokens], each token's row of cos and sin; NULL: its slot.
+ *   cu_new   : device [B + 1]; lens: device [B], tokens of each sequence in
+ *              the cache INCLUDING the new ones; token i of the n new ones of
+ *              sequence b goes to slot lens[b] - n + i.
+ *   table    : device [B][table_width]; slot s of sequence b is row s % page of
+ *              page table[b][s / page].  Entries behind a sequence are not read.
+ * The other slots of the cache and rows behind the last sequence are left as
+ * they were.  Two tokens must not share a slot.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA; on the device: LITE_ERR_DEVICE_CHECK. */
+typedef struct {
+    lite_attn_rows_t q, q_out, k, v;
+    void *k_pages, *v_pages;
+    int64_t pages;
+    const float *cos, *sin;
+    int64_t angle_rows;
+    const int32_t *positions, *cu_new, *lens, *table;
+    int32_t B, table_width, page, layout, rot, interleaved;
+} lite_attn_append_t;
+int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *args, void *stream);
+
+/* Attention of new tokens over the cache.
+ *   q, o     : [tokens][Hq][d] views; o must not overlap q, the cache or the
+ *              workspace.
+ *   lens     : device [B], keys of each sequence (the new tokens' own included,
+ *              appended before).  Cache, cu_new and table as above.
+ *   max_new  : an upper bound of the new tokens of a sequence, known to the
+ *              host; it only selects between kernels (any value is correct).
+ *   causal   : 0: every new token sees all of its sequence's keys (a frame that
+ *              attends to all of itself); otherwise as above.
+ *   scale    : factor of the logits, > 0 (1 / sqrt(d) usually).
+ *   workspace: device scratch of lite_attn_gqa_workspace bytes, 16-byte
+ *              aligned; free for reuse in stream order.
+ * Errors: INVALID_ARG, UNSUPPORTED (2^31 keys or query rows), CUDA; on the
+ * device: LITE_ERR_DEVICE_CHECK, LITE_ERR_DEVICE_TIMEOUT. */
+typedef struct {
+    lite_attn_rows_t q, o;
+    void *k_pages, *v_pages;
+    int64_t pages;
+    const int32_t *cu_new, *lens, *table;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t B, table_width, page, layout, max_new, causal;
+    float scale;
+    int32_t reserved;
+} lite_attn_attend_t;
+int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *args, void *stream);
+
+/* Attention over whole packed sequences.
+ *   q, o     : [tokens][Hq][d] views, sequence b in rows [cu_q[b], cu_q[b + 1]).
+ *   k, v     : [tokens][Hk][d] views, sequence b in rows [cu_k[b], cu_k[b + 1]);
+ *              cu_k may be cu_q.
+ *   The rest as for lite_attn_cache_attend. */
+typedef struct {
+    lite_attn_rows_t q, o, k, v;
+    const int32_t *cu_q, *cu_k;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t B, causal;
+    float scale;
+    int32_t reserved;
+} lite_attn_prompt_t;
+int lite_attn_prompt(lite_attn_gqa_t plan, const lite_attn_prompt_t *args, void *stream);
 
 /* Kernel launches issued by this library in the calling process so far. */
 int64_t lite_attn_launch_count(void);

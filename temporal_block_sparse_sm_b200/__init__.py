@@ -8,6 +8,7 @@ it does, and raises if it is missing.
 Modules: ``liteattn`` (the C ABI and the Plan / Mask objects), ``propagation``
 (mask propagation policies), ``calibration`` (per-step thresholds from error
 budgets), ``host_pipeline`` (steps on host-resident tensors with overlapped
-copies), ``synthetic`` (seeded video-token workloads).
+copies), ``serving`` (attention over packed prompts and over a paged cache, and
+the append that fills it), ``synthetic`` (seeded video-token workloads).
 """
-__all__ = ["liteattn", "synthetic", "propagation", "calibration", "host_pipeline"]
+__all__ = ["liteattn", "synthetic", "propagation", "calibration", "host_pipeline", "serving"]

@@ -35,7 +35,7 @@ def needs_build(lib: str = LIB) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, profile: bool = False, debug: bool = False) -> str:
-    """Compile csrc/liteattn.cu (and the headers it includes) into libliteattn.so.
+    """Compile csrc/*.cu (and the headers they include) into libliteattn.so.
 
     profile=True builds libliteattn_prof.so with per-CTA cycle counters instead;
     debug=True builds libliteattn_debug.so, whose attention kernel checks every
@@ -48,7 +48,7 @@ def build(force: bool = False, verbose: bool = False, profile: bool = False, deb
     flags = (["-DLITE_PROFILE"] if profile else []) + (["-DLITE_DEBUG_CHECKS"] if debug else [])
     cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
            "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
-           "-Xptxas", "-v" if verbose else "-O3"] + flags + [os.path.join(CSRC, "liteattn.cu"), "-o", tmp]
+           "-Xptxas", "-v" if verbose else "-O3"] + flags + ["--threads", "0"] + sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + ["-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)

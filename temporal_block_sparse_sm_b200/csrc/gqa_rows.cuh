@@ -1,0 +1,459 @@
+// gqa_rows.cuh -- grouped-query attention of a few query rows per key head (a decoding
+// step), over paged or packed keys, split along the keys; and the kernel that joins the
+// segments of split items.
+//
+//   o_r = sum_j 2^(c (q_r . k_j) - c m_r) v_j / sum_j 2^(c (q_r . k_j) - c m_r),
+//   c = scale log2 e,  j over the keys that row r sees.
+//
+// A work item is 16 query rows (token t, head g of the group; flattened t * G + g) of one
+// key head: all heads of a group share the keys that are read, and 16 is the M of
+// mma.sync.m16n8k16.  Bound by memory: per key 4 D bytes are read for 64 D operations, far
+// below what even the legacy tensor path delivers, so nothing is gained from 128-row
+// tcgen05 tiles of which one row in eight would be used.
+//
+// A block is four computing warps and one that issues TMA loads of 64-key tiles into a ring
+// (three stages of 32 KB at D = 128; two blocks per SM keep up to 192 KB in flight).  A
+// computing warp owns 16 keys of every tile and keeps its own running maximum, sum and
+// output, so warps meet only at the ring's barriers; their states are joined once at the
+// end.
+//
+// Values that no row sees (behind the last key, in a page's unused part) are zeroed in
+// shared memory before the product, since 0 * NaN is NaN.  Where some rows see a key that
+// others do not, and a value there is not finite, the product of those 16 keys is done
+// with scalar code that leaves hidden keys out.
+#pragma once
+
+#include "attn_kernel.cuh"   // WaitCtx, wait_bar, drain_wait
+#include "serving_internal.cuh"
+
+namespace lite {
+
+struct GqaParams {
+    GqaBatch b;
+    const uint16_t *q;
+    uint16_t *o;
+    int64_t q_st, q_sh, o_st, o_sh;   // token and head strides, elements
+    float scale_log2;                 // scale * log2 e
+    float *ws_o;                      // workspace: [slot][rows of an item][D] unnormalised outputs
+    float *ws_ml;                     // [slot][rows of an item][2]: running maximum (raw logit), sum
+};
+
+template <int D>
+struct RowsCfg {
+    static constexpr int BN = 64;               // keys of a tile
+    static constexpr int ROWS = 16;
+    static constexpr int NWARP = 4;             // computing warps
+    static constexpr int NTHREADS = 32 * (NWARP + 1);
+    static constexpr int DCH = D / 64;
+    static constexpr uint32_t KV_BYTES = BN * D * 2u;
+    static constexpr uint32_t CHUNK_BYTES = BN * 128u;
+    static constexpr int NST = D == 128 ? 3 : 6;
+    static constexpr uint32_t RING_BYTES = NST * 2u * KV_BYTES;
+    static constexpr int OSTRIDE = D + 4;       // floats, joins of the warps' outputs
+    static constexpr uint32_t SMEM_BYTES = RING_BYTES + 1024u;
+    static_assert(NWARP * ROWS * OSTRIDE * 4u <= RING_BYTES, "join buffer");
+};
+
+namespace ptx {
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+}  // namespace ptx
+
+// Where a tile's keys lie: one TMA box per page (or per tile, where a page holds it all).
+// Lane `lane` of the producing warp owns box `lane` of a tile and looks its page up ahead
+// of the wait for a free stage.
+template <int BN, int DCH>
+struct KvTiles {
+    const GqaBatch &p;
+    const WorkItem &w;
+    int box;      // rows of a box
+    int end;      // keys that any row of the item sees; boxes behind it are not loaded
+    __device__ __forceinline__ KvTiles(const GqaBatch &p_, const WorkItem &w_, int end_) : p(p_), w(w_), end(end_) {
+        const int page = p.mode == kKvPacked ? BN : 1 << p.page_shift;
+        box = page < BN ? page : BN;
+    }
+    __device__ __forceinline__ int boxes(int t) const {   // boxes of tile t that hold a key before `end`
+        const int left = end - t * BN;
+        return left >= BN ? BN / box : (left + box - 1) / box;
+    }
+    // the page of this lane's box of tile t (-1: the lane has none)
+    __device__ __forceinline__ int page_of(int t, int lane) const {
+        if (lane >= boxes(t)) return -1;
+        if (p.mode == kKvPacked) return 0;
+        const int pg = __ldg(p.table + static_cast<int64_t>(w.b) * p.table_w + ((t * BN + lane * box) >> p.page_shift));
+        if (pg >= 0 && pg < p.pages) return pg;
+        atomicExch(p.status, kStatusCheck);
+        return static_cast<int>(p.pages);   // outside the tensor map: reads as zeros
+    }
+    __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap *m, uint32_t bar, int t, int lane, int pg) const {
+        if (pg < 0) return;
+        const int j = t * BN + lane * box;
+        const int row = p.mode == kKvPacked ? static_cast<int>(w.s.k0) + j : j & ((1 << p.page_shift) - 1);
+#pragma unroll
+        for (int c = 0; c < DCH; ++c) {
+            const uint32_t at = dst + c * (BN * 128u) + static_cast<uint32_t>(lane * box) * 128u;
+            if (p.mode == kKvPagesBhnd) ptx::tma_load_4d(at, m, bar, c * 64, row, w.h, pg);
+            else ptx::tma_load_4d(at, m, bar, c * 64, w.h, row, pg);
+        }
+    }
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(RowsCfg<D>::NTHREADS, 2)
+gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
+    using C = RowsCfg<D>;
+    constexpr int BN = C::BN, NST = C::NST, DCH = C::DCH;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * NST];
+    __shared__ ScanScratch scan;
+    __shared__ float s_ml[C::NWARP][C::ROWS][2];
+    __shared__ uint32_t s_abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw_s = ptx::smem_u32(smem_raw);
+    const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - raw_s);
+    auto full = [&](int st) { return ptx::smem_u32(bars + st); };
+    auto empty = [&](int st) { return ptx::smem_u32(bars + NST + st); };
+
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < NST; ++st) {
+            ptx::mbar_init(full(st), 1);
+            ptx::mbar_init(empty(st), C::NWARP);
+        }
+        s_abort = 0u;
+        ptx::fence_barrier_init();
+    }
+    WorkItem w;
+    const bool any = find_work<C::NTHREADS, true>(p.b, blockIdx.x, scan, w);
+    __syncthreads();
+    if (!any) return;
+
+    const int G = p.b.G;
+    const int row0 = w.i * C::ROWS, nrows = min(C::ROWS, w.s.n * G - row0);
+    const int lim_lo = visible_keys(p.b, w.s, row0 / G), lim_hi = visible_keys(p.b, w.s, (row0 + nrows - 1) / G);
+    const int t_lo = w.seg * w.L;
+    const int t_end = (lim_hi + BN - 1) / BN;
+    const int t_hi = w.L >= t_end - t_lo ? t_end : t_lo + w.L;   // t_hi <= t_lo: an empty segment
+    if (t_hi <= t_lo && w.segs > 1) return;                      // the join does not read it
+    const WaitCtx wctx{&s_abort, p.b.status};
+
+    if (warp == C::NWARP) {
+        // ------------------------------------------------------------ loads
+        KvTiles<BN, DCH> kv(p.b, w, lim_hi);
+        int pg = t_lo < t_hi ? kv.page_of(t_lo, lane) : -1;
+        int issued = t_lo;
+        for (int t = t_lo; t < t_hi; ++t) {
+            const int e = t - t_lo, st = e % NST;
+            const int next = t + 1 < t_hi ? kv.page_of(t + 1, lane) : -1;
+            if (!__all_sync(0xFFFFFFFFu, wait_bar(empty(st), ((e / NST) & 1) ^ 1u, wctx))) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), kv.boxes(t) * kv.box * D * 4u);
+            __syncwarp();
+            const uint32_t dst = base_s + st * 2u * C::KV_BYTES;
+            kv.load(dst, &tm_k, full(st), t, lane, pg);
+            kv.load(dst + C::KV_BYTES, &tm_v, full(st), t, lane, pg);
+            __syncwarp();
+            pg = next;
+            issued = t + 1;
+        }
+        // every copy that this block started lands before it exits
+        for (int e = max(0, issued - t_lo - NST); e < issued - t_lo; ++e) drain_wait(full(e % NST), (e / NST) & 1);
+        return;
+    }
+
+    // ---------------------------------------------------------------- computing warps
+    const int gid = lane >> 2, tig = lane & 3;
+    // the thread's two rows (of the item's 16): gid and gid + 8
+    int lim[2];
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = gid + 8 * r;
+        const bool ok = row < nrows;
+        const int t = ok ? (row0 + row) / G : 0, g = ok ? (row0 + row) % G : 0;
+        lim[r] = ok ? visible_keys(p.b, w.s, t) : 0;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (static_cast<int64_t>(w.s.q0) + t) * p.q_st +
+                                                                 (static_cast<int64_t>(w.h) * G + g) * p.q_sh);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            qf[kk][r] = ok ? __ldg(src + kk * 8 + tig) : 0u;
+            qf[kk][2 + r] = ok ? __ldg(src + kk * 8 + 4 + tig) : 0u;
+        }
+    }
+    const float cl2 = p.scale_log2;
+    const float resc = 8.0f / cl2;    // the reference moves when the maximum rose by over 2^8 in weight
+    float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float acc[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+
+    // ldmatrix rows of this lane: matrix lane/8, row lane%8 of it
+    const int mi = lane >> 3, mr = lane & 7;
+    for (int t = t_lo; t < t_hi; ++t) {
+        const int e = t - t_lo, st = e % NST;
+        const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(full(st), (e / NST) & 1, wctx));
+        const int kb = t * BN + warp * 16;             // the warp's first key
+        if (ok && kb < lim_hi) {
+            const uint32_t kt = base_s + st * 2u * C::KV_BYTES, vt = kt + C::KV_BYTES;
+            float sc[2][4] = {};
+            {
+                // matrices: (keys 0-7, d 0-7), (keys 0-7, d 8-15), (keys 8-15, d 0-7), (keys 8-15, d 8-15)
+                const int key = warp * 16 + (mi >> 1) * 8 + mr;
+                const uint32_t rowa = kt + key * 128u;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t c16 = (kk & 3) * 2 + (mi & 1);
+                    uint32_t b0, b1, b2, b3;
+                    ptx::ldsm4(rowa + (kk >> 2) * C::CHUNK_BYTES + ((c16 ^ (key & 7)) << 4), b0, b1, b2, b3);
+                    ptx::mma16816<F16>(sc[0], qf[kk], b0, b1);
+                    ptx::mma16816<F16>(sc[1], qf[kk], b2, b3);
+                }
+            }
+            const bool masked = kb + 16 > lim_lo;       // some row does not see all of these keys
+            bool scalar = false;
+            if (masked) {
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (kb + nb * 8 + 2 * tig + (j & 1) >= lim[j >> 1]) sc[nb][j] = -INFINITY;
+                uint32_t bad = 0;
+                for (int x = lane; x < 16 * DCH * 8; x += 32) {   // 16-byte pieces of the 16 value rows
+                    const int key = x / (DCH * 8), c = (x / 8) % DCH, piece = x % 8;
+                    uint4 *at = reinterpret_cast<uint4 *>(base + (vt - base_s) + c * C::CHUNK_BYTES +
+                                                          (warp * 16 + key) * 128u + piece * 16u);
+                    if (kb + key >= lim_hi) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (kb + key >= lim_lo) {
+                        const uint4 v = *at;
+                        bad |= nonfinite16<F16>(v.x) | nonfinite16<F16>(v.y) | nonfinite16<F16>(v.z) | nonfinite16<F16>(v.w);
+                    }
+                }
+                scalar = __any_sync(0xFFFFFFFFu, bad != 0u);
+                __syncwarp();
+            }
+            float alpha[2];
+            bool moved = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+                alpha[r] = 1.0f;
+                if (mx - m_ref[r] > resc) {             // also the row's first finite maximum
+                    alpha[r] = ptx::ex2((m_ref[r] - mx) * cl2);
+                    m_ref[r] = mx;
+                    l[r] *= alpha[r];
+                    moved = true;
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    acc[n][0] *= alpha[0], acc[n][1] *= alpha[0];
+                    acc[n][2] *= alpha[1], acc[n][3] *= alpha[1];
+                }
+            }
+            // weights, rounded to 16 bits for the product; the sum adds the rounded ones
+            float neg[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) neg[r] = m_ref[r] == -INFINITY ? 0.0f : -m_ref[r] * cl2;
+            uint32_t pf[4];
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = ptx::ex2(fmaf(sc[nb][2 * r], cl2, neg[r])), p1 = ptx::ex2(fmaf(sc[nb][2 * r + 1], cl2, neg[r]));
+                    pf[nb * 2 + r] = pack16<F16>(p0, p1);
+                    float a = 0.0f, b = 0.0f;
+                    add16x2<F16>(a, b, pf[nb * 2 + r]);
+                    l[r] += a + b;
+                }
+            if (!scalar) {
+                // matrices of V: (keys 0-7, d n..n+7), (keys 8-15, same d), then the next 8 d
+                const int key = warp * 16 + (mi & 1) * 8 + mr;
+                const uint32_t rowa = vt + key * 128u;
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    const uint32_t c16 = (n & 3) * 2 + (mi >> 1);
+                    uint32_t b0, b1, b2, b3;
+                    ptx::ldsm4t(rowa + (n >> 2) * C::CHUNK_BYTES + ((c16 ^ (key & 7)) << 4), b0, b1, b2, b3);
+                    ptx::mma16816<F16>(acc[2 * n], pf, b0, b1);
+                    ptx::mma16816<F16>(acc[2 * n + 1], pf, b2, b3);
+                }
+            } else {
+#pragma unroll 1
+                for (int key = 0; key < 16; ++key) {
+                    const int from = (lane & ~3) | ((key & 7) >> 1);   // the lane holding this key's weights
+                    float wt[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float a = 0.0f, b = 0.0f;
+                        add16x2<F16>(a, b, __shfl_sync(0xFFFFFFFFu, key < 8 ? pf[r] : pf[2 + r], from));
+                        wt[r] = (key & 1) ? b : a;
+                    }
+                    const bool see0 = kb + key < lim[0], see1 = kb + key < lim[1];
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        const uint32_t at = (n >> 3) * C::CHUNK_BYTES + (warp * 16 + key) * 128u + (((n & 7) ^ (key & 7)) << 4) + tig * 4u;
+                        float v0, v1;
+                        unpack16<F16>(*reinterpret_cast<const uint32_t *>(base + (vt - base_s) + at), v0, v1);
+                        if (see0) acc[n][0] += wt[0] * v0, acc[n][1] += wt[0] * v1;
+                        if (see1) acc[n][2] += wt[1] * v0, acc[n][3] += wt[1] * v1;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty(st));
+    }
+
+    // ---------------------------------------------------------------- join of the four warps
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+        if (tig == 0) {
+            s_ml[warp][gid + 8 * r][0] = m_ref[r];
+            s_ml[warp][gid + 8 * r][1] = l[r];
+        }
+    }
+    ptx::bar_sync(1, 32 * C::NWARP);   // also: every warp has read its last tile, the ring is free
+    float *ob = reinterpret_cast<float *>(base);
+    float f[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < C::NWARP; ++k) mx = fmaxf(mx, s_ml[k][gid + 8 * r][0]);
+        f[r] = m_ref[r] == -INFINITY ? 0.0f : ptx::ex2((m_ref[r] - mx) * cl2);
+        if (m_ref[r] != m_ref[r]) f[r] = m_ref[r];   // NaN logits stay NaN
+    }
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+        float *at = ob + (warp * C::ROWS + gid) * C::OSTRIDE + n * 8 + 2 * tig;
+        *reinterpret_cast<float2 *>(at) = make_float2(acc[n][0] * f[0], acc[n][1] * f[0]);
+        *reinterpret_cast<float2 *>(at + 8 * C::OSTRIDE) = make_float2(acc[n][2] * f[1], acc[n][3] * f[1]);
+    }
+    ptx::bar_sync(1, 32 * C::NWARP);
+    constexpr int CPT = D / 8;          // columns per thread: 16 rows x 8 threads
+    const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * CPT;
+    if (row < nrows) {
+        float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < C::NWARP; ++k) mx = fmaxf(mx, s_ml[k][row][0]);
+#pragma unroll
+        for (int k = 0; k < C::NWARP; ++k) {
+            const float mk = s_ml[k][row][0];
+            if (mk != -INFINITY) sum += s_ml[k][row][1] * ptx::ex2((mk - mx) * cl2);
+        }
+        float v[CPT];
+#pragma unroll
+        for (int c = 0; c < CPT; c += 4) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < C::NWARP; ++k) {
+                const float4 b = *reinterpret_cast<const float4 *>(ob + (k * C::ROWS + row) * C::OSTRIDE + col + c);
+                a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+            }
+            v[c] = a.x, v[c + 1] = a.y, v[c + 2] = a.z, v[c + 3] = a.w;
+        }
+        const int t = (row0 + row) / G, g = (row0 + row) % G;
+        if (w.segs == 1) {
+            // a row that sees no key is zero; one whose visible logits are all -inf is 0 / 0
+            const float inv = visible_keys(p.b, w.s, t) == 0 ? 0.0f : 1.0f / sum;
+            uint32_t pk[CPT / 2];
+#pragma unroll
+            for (int c = 0; c < CPT / 2; ++c) pk[c] = pack16<F16>(v[2 * c] * inv, v[2 * c + 1] * inv);
+            uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st +
+                                                   (static_cast<int64_t>(w.h) * G + g) * p.o_sh + col);
+#pragma unroll
+            for (int c = 0; c < CPT / 8; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        } else {
+            const int64_t at = static_cast<int64_t>(w.slot) * C::ROWS + row;
+            float4 *dst = reinterpret_cast<float4 *>(p.ws_o + at * D + col);
+#pragma unroll
+            for (int c = 0; c < CPT / 4; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            if ((threadIdx.x & 7) == 0) *reinterpret_cast<float2 *>(p.ws_ml + 2 * at) = make_float2(mx, sum);
+        }
+    }
+}
+
+// Joins the segments of split items: a warp per row, over the item's segments
+//   o = sum_s 2^(c (m_s - m)) O_s / sum_s 2^(c (m_s - m)) l_s.
+// Grid: (items, row groups of four).  Items of one segment have written their output.
+constexpr int kJoinThreads = 128;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams p, int rows_per_item, int slot_tokens) {
+    __shared__ ScanScratch scan;
+    WorkItem w;
+    if (!find_work<kJoinThreads, false>(p.b, blockIdx.x, scan, w) || w.segs <= 1) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.y * (kJoinThreads / 32) + warp, G = p.b.G;
+    // the item's rows: flattened (token, head), or per slot of slot_tokens tokens in 128 rows
+    int t, g, t_last;
+    if (p.b.unit_rows) {
+        const int r = w.i * p.b.unit_rows + row;
+        t = r / G, g = r % G;
+        t_last = static_cast<int>((min(static_cast<int64_t>(w.i + 1) * p.b.unit_rows, static_cast<int64_t>(w.s.n) * G) - 1) / G);
+        if (row >= p.b.unit_rows) return;
+    } else {
+        const int r = row & 127;
+        if (r >= slot_tokens * G) return;
+        t = w.i * p.b.unit_tokens + (row >> 7) * slot_tokens + r / G, g = r % G;
+        t_last = min((w.i + 1) * p.b.unit_tokens, w.s.n) - 1;
+    }
+    if (t >= w.s.n) return;
+    const int vis = visible_keys(p.b, w.s, t);
+    const int t_end = (visible_keys(p.b, w.s, t_last) + p.b.tile - 1) / p.b.tile;
+    const int segs = t_end > 0 ? (t_end + w.L - 1) / w.L : 0;     // segments that were written
+    const int64_t first = static_cast<int64_t>(w.slot) * rows_per_item + row;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
+    float mx = -INFINITY;
+    for (int s = lane; s < segs; s += 32) mx = fmaxf(mx, ml[first + static_cast<int64_t>(s) * rows_per_item].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    constexpr int CPT = D / 32;
+    float a[CPT] = {}, sum = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < segs; ++s) {
+        const int64_t at = first + static_cast<int64_t>(s) * rows_per_item;
+        const float2 x = ml[at];
+        const float f = x.x == -INFINITY ? 0.0f : ptx::ex2((x.x - mx) * p.scale_log2);
+        const float *src = p.ws_o + at * D + lane * CPT;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) a[c] += f * src[c];
+        sum += f * x.y;
+    }
+    const float inv = vis == 0 ? 0.0f : 1.0f / sum;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st +
+                                                 (static_cast<int64_t>(w.h) * G + g) * p.o_sh + lane * CPT);
+#pragma unroll
+    for (int c = 0; c < CPT / 2; ++c) dst[c] = pack16<F16>(a[2 * c] * inv, a[2 * c + 1] * inv);
+}
+
+}  // namespace lite

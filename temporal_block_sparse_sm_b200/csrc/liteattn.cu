@@ -3,12 +3,10 @@
 // launches of the sm_100a kernels.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -16,6 +14,7 @@
 
 #include "liteattn.h"
 #include "attn_kernel.cuh"
+#include "host_util.cuh"
 #include "liteattn_internal.cuh"
 #include "mask_kernels.cuh"
 #include "metric_kernels.cuh"
@@ -26,80 +25,6 @@ namespace {
 
 constexpr uint32_t kPlanMagic = 0x4C415050u;  // "LAPP"
 constexpr uint32_t kMaskMagic = 0x4C414D4Bu;  // "LAMK"
-
-std::atomic<int64_t> g_launches{0};
-
-// NVTX range for the duration of a scope: the host side of each call shows up
-// on profiler timelines (header-only NVTX3; a no-op without a tool attached).
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
-
-// Makes a plan's device current for the duration of a call and gives the caller
-// back its own current device on exit, so a plan works whichever device the
-// calling thread has selected (kernels, copies, events and synchronisation all
-// go to the device that owns the plan's memory).
-struct DeviceScope {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceScope(int device) {
-        if (cudaGetDevice(&prev) != cudaSuccess) {
-            cudaGetLastError();
-            prev = -1;
-            return;
-        }
-        ok = prev == device || cudaSetDevice(device) == cudaSuccess;
-    }
-    ~DeviceScope() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-    DeviceScope(const DeviceScope &) = delete;
-    DeviceScope &operator=(const DeviceScope &) = delete;
-};
-
-constexpr int kMaxDevices = 64;
-
-// Fault injection for tests: LITE_ATTN_FAULT=alloc|launch|status makes the
-// matching host path report its error without touching the GPU;
-// LITE_ATTN_FAULT=device_wait makes the attention kernel's first CTA wait on a
-// barrier that nothing arrives on, so its bounded wait runs out and the step
-// reports LITE_ERR_DEVICE_TIMEOUT through the status word.
-bool fault(const char *what) {
-    const char *e = std::getenv("LITE_ATTN_FAULT");
-    return e && std::strcmp(e, what) == 0;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-using AddrRangeFn = CUresult (*)(CUdeviceptr *, size_t *, CUdeviceptr);
-
-struct DriverFns {
-    EncodeTiledFn encode = nullptr;
-    AddrRangeFn addr_range = nullptr;
-    bool ok = false;
-};
-
-const DriverFns &driver() {
-    static DriverFns fns;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        cudaDriverEntryPointQueryResult q1, q2;
-        void *p1 = nullptr, *p2 = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p1, cudaEnableDefault, &q1) == cudaSuccess &&
-            q1 == cudaDriverEntryPointSuccess)
-            fns.encode = reinterpret_cast<EncodeTiledFn>(p1);
-        if (cudaGetDriverEntryPoint("cuMemGetAddressRange", &p2, cudaEnableDefault, &q2) == cudaSuccess &&
-            q2 == cudaDriverEntryPointSuccess)
-            fns.addr_range = reinterpret_cast<AddrRangeFn>(p2);
-        fns.ok = fns.encode && fns.addr_range;
-    });
-    return fns;
-}
 
 struct TimingRec {
     cudaEvent_t a0, a1, s0, s1;
@@ -169,28 +94,8 @@ struct lite_attn_mask {
 
 namespace {
 
-int cuda_err(cudaError_t e) { return e == cudaSuccess ? LITE_OK : LITE_ERR_CUDA; }
-
 bool valid_plan(const lite_attn_plan *p) { return p && p->magic == kPlanMagic; }
 bool valid_mask(const lite_attn_mask *m) { return m && m->magic == kMaskMagic; }
-
-// Checks that [ptr, ptr + bytes) is device memory of `device` inside one allocation,
-// and that ptr is aligned to `align` bytes (a power of two).
-bool device_range_ok(const void *ptr, size_t bytes, int device, uintptr_t align = 16) {
-    if (!ptr || (reinterpret_cast<uintptr_t>(ptr) & (align - 1u))) return false;
-    cudaPointerAttributes attr;
-    if (cudaPointerGetAttributes(&attr, ptr) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) return false;
-    if (attr.type == cudaMemoryTypeDevice && attr.device != device) return false;
-    CUdeviceptr basep = 0;
-    size_t size = 0;
-    if (driver().addr_range(&basep, &size, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS) return false;
-    const uintptr_t b = static_cast<uintptr_t>(basep), x = reinterpret_cast<uintptr_t>(ptr);
-    return x >= b && x - b + bytes <= size;
-}
 
 // Bytes from the plan's first element to one past its last one in a tensor of Ht heads.
 size_t tensor_extent_bytes(const Geometry &g) {

@@ -1,0 +1,408 @@
+// serving.cu -- host side of the serving attention calls of include/liteattn.h: the
+// grouped-query plan, its argument checks, tensor maps and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <new>
+
+#include "liteattn.h"
+#include "gqa_rows.cuh"
+#include "host_util.cuh"
+#include "rope_append.cuh"
+#include "serving_internal.cuh"
+
+using namespace lite;
+
+namespace {
+constexpr uint32_t kGqaMagic = 0x4C414751u;  // "LAGQ"
+}
+
+struct lite_attn_gqa {
+    uint32_t magic;
+    int Hq, Hk, d, dtype;
+    int device;
+    int sms;
+    int32_t *status;   // device status word (sticky)
+};
+
+namespace {
+
+bool valid_gqa(const lite_attn_gqa *p) { return p && p->magic == kGqaMagic; }
+
+// A [tokens][heads][d] view: what it spans, and that the kernels can address it.
+bool rows_ok(const lite_attn_rows_t &r, int heads, int d, int device) {
+    if (r.tokens < 0 || r.tokens >= (int64_t(1) << 31)) return false;
+    if (r.tokens == 0) return true;
+    if (!r.ptr || r.stride_token < d || r.stride_head < d || r.stride_token % 8 || r.stride_head % 8) return false;
+    if (r.stride_token >= (int64_t(1) << 31) || r.stride_head >= (int64_t(1) << 31)) return false;
+    const size_t elems = static_cast<size_t>(r.tokens - 1) * r.stride_token + static_cast<size_t>(heads - 1) * r.stride_head + d;
+    return device_range_ok(r.ptr, elems * 2u, device);
+}
+size_t rows_bytes(const lite_attn_rows_t &r, int heads, int d) {
+    if (r.tokens == 0) return 0;
+    return 2u * (static_cast<size_t>(r.tokens - 1) * r.stride_token + static_cast<size_t>(heads - 1) * r.stride_head + d);
+}
+bool apart(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na == 0 || nb == 0 || x + na <= y || y + nb <= x;
+}
+
+struct CacheView {
+    const void *k, *v;
+    int64_t pages;
+    int page, layout;
+};
+int log2_page(int page) {   // -1 unless a power of two from 16 to 65536
+    for (int s = 4; s <= 16; ++s)
+        if (page == 1 << s) return s;
+    return -1;
+}
+size_t cache_bytes(const lite_attn_gqa *pl, const CacheView &c) {
+    return 2u * static_cast<size_t>(c.pages) * c.page * pl->Hk * pl->d;
+}
+int check_cache(const lite_attn_gqa *pl, const CacheView &c) {
+    if (c.layout != LITE_LAYOUT_BHND && c.layout != LITE_LAYOUT_BNHD) return LITE_ERR_INVALID_ARG;
+    if (c.pages < 1 || c.pages >= (int64_t(1) << 31)) return LITE_ERR_INVALID_ARG;
+    if (log2_page(c.page) < 0) return LITE_ERR_UNSUPPORTED;
+    const size_t bytes = cache_bytes(pl, c);
+    if (!device_range_ok(c.k, bytes, pl->device) || !device_range_ok(c.v, bytes, pl->device)) return LITE_ERR_INVALID_ARG;
+    return apart(c.k, bytes, c.v, bytes) ? LITE_OK : LITE_ERR_INVALID_ARG;
+}
+
+bool ints_ok(const int32_t *p, size_t n, int device) { return device_range_ok(p, n * 4u, device, 4); }
+
+// k or v as a 4-D tensor map of 64-element columns, 128-byte swizzle: pages as
+// (d, row, head, page) or (d, head, row, page), packed rows as (d, head, row, 1).
+bool encode_kv(CUtensorMap *m, const lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *r, int box_rows) {
+    const cuuint64_t d = static_cast<cuuint64_t>(pl->d), H = static_cast<cuuint64_t>(pl->Hk);
+    const cuuint32_t rows = static_cast<cuuint32_t>(box_rows);
+    cuuint64_t dims[4] = {d, H, 1, 1}, strides[3];
+    cuuint32_t box[4] = {64u, 1u, rows, 1u};
+    const void *ptr;
+    if (c) {
+        const cuuint64_t P = static_cast<cuuint64_t>(c->page);
+        ptr = c->k;
+        dims[3] = static_cast<cuuint64_t>(c->pages);
+        strides[2] = 2u * P * H * d;
+        if (c->layout == LITE_LAYOUT_BHND) {
+            dims[1] = P, dims[2] = H;
+            strides[0] = 2u * d, strides[1] = 2u * P * d;
+            box[1] = rows, box[2] = 1u;
+        } else {
+            dims[2] = P;
+            strides[0] = 2u * d, strides[1] = 2u * H * d;
+        }
+    } else {
+        ptr = r->ptr;
+        dims[2] = static_cast<cuuint64_t>(r->tokens);
+        strides[0] = 2u * static_cast<cuuint64_t>(r->stride_head);
+        strides[1] = 2u * static_cast<cuuint64_t>(r->stride_token);
+        strides[2] = strides[1] * dims[2];
+    }
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return driver().encode(m, pl->dtype == LITE_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Raises a kernel's dynamic shared-memory limit once per device.
+template <typename K>
+int allow_smem(K kernel, std::atomic<bool> *done, int device, uint32_t bytes) {
+    if (device < 0 || device >= kMaxDevices) return LITE_ERR_CUDA;
+    if (done[device].load(std::memory_order_acquire)) return LITE_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
+        cudaGetLastError();
+        return LITE_ERR_CUDA;
+    }
+    done[device].store(true, std::memory_order_release);
+    return LITE_OK;
+}
+
+// How a batch is divided among blocks: decided from what the host knows (tensor sizes).
+struct Division {
+    int64_t items;        // most work items there can be
+    int target;           // split target, 0: no splitting
+    size_t workspace;
+};
+constexpr int kRowsMinTiles = 4;      // shortest segment, tiles of 64 keys
+
+Division divide_rows(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_keys) {
+    const int64_t G = pl->Hq / pl->Hk, rows = RowsCfg<128>::ROWS;
+    Division dv;
+    dv.items = pl->Hk * std::min((tokens * G + B * (rows - 1)) / rows, tokens * G);
+    const int target = 2 * pl->sms;   // two blocks per SM
+    const int64_t least = pl->Hk * ((tokens * G + rows - 1) / rows);   // items of a batch without padding
+    dv.target = (least >= 2 * target || max_keys <= kRowsMinTiles * RowsCfg<128>::BN) ? 0 : target;
+    dv.workspace = dv.target ? static_cast<size_t>(2 * dv.target) * rows * (pl->d + 2) * 4u : 0;
+    return dv;
+}
+
+template <int D, bool F16>
+int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMap &tv, GqaParams &p, const Division &dv,
+                cudaStream_t s) {
+    using C = RowsCfg<D>;
+    static std::atomic<bool> done[kMaxDevices];
+    int rc = allow_smem(gqa_rows_kernel<D, F16>, done, pl->device, C::SMEM_BYTES);
+    if (rc != LITE_OK) return rc;
+    gqa_rows_kernel<D, F16><<<static_cast<unsigned>(dv.items + dv.target), C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
+    g_launches.fetch_add(1);
+    if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target) return rc;
+    gqa_join_kernel<D, F16><<<dim3(static_cast<unsigned>(dv.items), C::ROWS / 4), kJoinThreads, 0, s>>>(p, C::ROWS, 0);
+    g_launches.fetch_add(1);
+    return cuda_err(cudaGetLastError());
+}
+
+// Attention of q over the cache (c) or packed rows (k, v).
+int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, const lite_attn_rows_t *v,
+              const lite_attn_rows_t &q, const lite_attn_rows_t &o, GqaBatch b, float scale, void *workspace,
+              size_t workspace_bytes, cudaStream_t s) {
+    const int G = pl->Hq / pl->Hk;
+    const int64_t max_keys = c ? b.max_keys : b.Tk;
+    const Division dv = divide_rows(pl, b.B, q.tokens, max_keys);
+    if (dv.items + dv.target >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
+    if (workspace_bytes < dv.workspace) return LITE_ERR_INVALID_ARG;
+    if (dv.workspace && !device_range_ok(workspace, dv.workspace, pl->device)) return LITE_ERR_INVALID_ARG;
+    if (dv.workspace && !apart(workspace, dv.workspace, o.ptr, rows_bytes(o, pl->Hq, pl->d))) return LITE_ERR_INVALID_ARG;
+    if (fault("launch")) return LITE_ERR_CUDA;
+    b.G = G;
+    b.Hk = pl->Hk;
+    b.status = pl->status;
+    b.unit_rows = RowsCfg<128>::ROWS;
+    b.unit_tokens = 0;
+    b.tile = RowsCfg<128>::BN;
+    b.split_target = dv.target;
+    b.min_tiles = kRowsMinTiles;
+    GqaParams p;
+    p.b = b;
+    p.q = static_cast<const uint16_t *>(q.ptr);
+    p.o = static_cast<uint16_t *>(o.ptr);
+    p.q_st = q.stride_token, p.q_sh = q.stride_head, p.o_st = o.stride_token, p.o_sh = o.stride_head;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.ws_ml = static_cast<float *>(workspace);
+    p.ws_o = p.ws_ml + static_cast<size_t>(2 * dv.target) * b.unit_rows * 2;
+    const int box = c ? std::min(c->page, b.tile) : b.tile;
+    CUtensorMap tk, tv;
+    std::memset(&tk, 0, sizeof tk);
+    std::memset(&tv, 0, sizeof tv);
+    if (c) {
+        CacheView cv = *c;
+        cv.k = c->v;
+        if (!encode_kv(&tk, pl, c, nullptr, box) || !encode_kv(&tv, pl, &cv, nullptr, box)) return LITE_ERR_CUDA;
+    } else if (k->tokens > 0) {   // without keys nothing is loaded
+        if (!encode_kv(&tk, pl, nullptr, k, box) || !encode_kv(&tv, pl, nullptr, v, box)) return LITE_ERR_CUDA;
+    }
+    const bool f16 = pl->dtype == LITE_DTYPE_FP16;
+    if (pl->d == 64) return f16 ? launch_rows<64, true>(pl, tk, tv, p, dv, s) : launch_rows<64, false>(pl, tk, tv, p, dv, s);
+    return f16 ? launch_rows<128, true>(pl, tk, tv, p, dv, s) : launch_rows<128, false>(pl, tk, tv, p, dv, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int lite_attn_gqa_create(lite_attn_gqa_t *out, int Hq, int Hk, int d, int dtype) {
+    if (!out) return LITE_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (Hq < 1 || Hk < 1 || Hq % Hk || d < 1) return LITE_ERR_INVALID_ARG;
+    if (dtype != LITE_DTYPE_BF16 && dtype != LITE_DTYPE_FP16) return LITE_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || Hq / Hk > 128 || Hq > 65536) return LITE_ERR_UNSUPPORTED;
+    if (fault("alloc")) return LITE_ERR_ALLOC;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LITE_ERR_CUDA;
+    int major = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return LITE_ERR_CUDA;
+    if (major != 10 || !driver().ok) return LITE_ERR_CUDA;
+    lite_attn_gqa *pl = new (std::nothrow) lite_attn_gqa();
+    if (!pl) return LITE_ERR_ALLOC;
+    pl->Hq = Hq, pl->Hk = Hk, pl->d = d, pl->dtype = dtype, pl->device = dev, pl->sms = sms;
+    if (cudaMalloc(&pl->status, 256) != cudaSuccess) {
+        cudaGetLastError();
+        delete pl;
+        return LITE_ERR_ALLOC;
+    }
+    if (cudaMemset(pl->status, 0, 256) != cudaSuccess) {
+        cudaFree(pl->status);
+        delete pl;
+        return LITE_ERR_CUDA;
+    }
+    pl->magic = kGqaMagic;
+    *out = pl;
+    return LITE_OK;
+}
+
+int lite_attn_gqa_destroy(lite_attn_gqa_t plan) {
+    if (!plan) return LITE_OK;
+    if (!valid_gqa(plan)) return LITE_ERR_INVALID_ARG;
+    DeviceScope ds(plan->device);
+    cudaDeviceSynchronize();
+    cudaFree(plan->status);
+    plan->magic = 0;
+    delete plan;
+    return LITE_OK;
+}
+
+int lite_attn_gqa_status(lite_attn_gqa_t plan, void *stream) {
+    if (!valid_gqa(plan)) return LITE_ERR_INVALID_ARG;
+    if (fault("status")) return LITE_ERR_DEVICE_TIMEOUT;
+    DeviceScope ds(plan->device);
+    if (!ds.ok) return LITE_ERR_CUDA;
+    int32_t status = LITE_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int rc = cuda_err(cudaMemcpyAsync(&status, plan->status, sizeof status, cudaMemcpyDeviceToHost, s));
+    if (rc == LITE_OK) rc = cuda_err(cudaStreamSynchronize(s));
+    if (rc != LITE_OK) return rc;
+    return status == LITE_OK ? LITE_OK : status == LITE_ERR_DEVICE_CHECK ? LITE_ERR_DEVICE_CHECK : LITE_ERR_DEVICE_TIMEOUT;
+}
+
+int lite_attn_gqa_workspace(lite_attn_gqa_t plan, int B, int64_t tokens, int max_new, int64_t max_keys, size_t *bytes) {
+    if (!valid_gqa(plan) || !bytes || B < 0 || tokens < 0 || max_new < 0 || max_keys < 0) return LITE_ERR_INVALID_ARG;
+    *bytes = divide_rows(plan, B, tokens, max_keys).workspace;
+    return LITE_OK;
+}
+
+int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *a, void *stream) {
+    if (!valid_gqa(plan) || !a || a->B < 0 || a->table_width < 1) return LITE_ERR_INVALID_ARG;
+    const int dev = plan->device, d = plan->d;
+    const bool has_q = a->q.ptr != nullptr;
+    if (a->k.tokens != a->v.tokens || (has_q && (a->q.tokens != a->k.tokens || a->q_out.tokens != a->k.tokens)) ||
+        (!has_q && a->q_out.ptr))
+        return LITE_ERR_INVALID_ARG;
+    if ((a->cos == nullptr) != (a->sin == nullptr) || (!a->cos && a->positions)) return LITE_ERR_INVALID_ARG;
+    if (a->cos && (a->rot < 16 || a->rot > d || a->rot % 16 || a->angle_rows < 1 || a->angle_rows >= (int64_t(1) << 31)))
+        return LITE_ERR_INVALID_ARG;
+    const CacheView c{a->k_pages, a->v_pages, a->pages, a->page, a->layout};
+    DeviceScope ds(dev);
+    if (!ds.ok) return LITE_ERR_CUDA;
+    int rc = check_cache(plan, c);
+    if (rc != LITE_OK) return rc;
+    if (a->k.tokens == 0 || a->B == 0) return LITE_OK;
+    if (!rows_ok(a->k, plan->Hk, d, dev) || !rows_ok(a->v, plan->Hk, d, dev) ||
+        (has_q && (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->q_out, plan->Hq, d, dev))))
+        return LITE_ERR_INVALID_ARG;
+    if (!ints_ok(a->cu_new, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->lens, a->B, dev) ||
+        !ints_ok(a->table, static_cast<size_t>(a->B) * a->table_width, dev) ||
+        (a->positions && !ints_ok(a->positions, a->k.tokens, dev)))
+        return LITE_ERR_INVALID_ARG;
+    if (a->cos) {
+        const size_t nb = static_cast<size_t>(a->angle_rows) * (a->rot / 2) * 4u;
+        if (!device_range_ok(a->cos, nb, dev) || !device_range_ok(a->sin, nb, dev)) return LITE_ERR_INVALID_ARG;
+    }
+    // the outputs overlap no input and not one another; q may be rotated in place
+    const size_t cb = cache_bytes(plan, c);
+    const lite_attn_rows_t *in[3] = {&a->k, &a->v, &a->q};
+    const bool in_place = has_q && a->q.ptr == a->q_out.ptr && a->q.stride_token == a->q_out.stride_token &&
+                          a->q.stride_head == a->q_out.stride_head;
+    for (int i = 0; i < (has_q ? 3 : 2); ++i) {
+        const size_t nb = rows_bytes(*in[i], i == 2 ? plan->Hq : plan->Hk, d);
+        if (!apart(in[i]->ptr, nb, c.k, cb) || !apart(in[i]->ptr, nb, c.v, cb)) return LITE_ERR_INVALID_ARG;
+        if (has_q && !in_place && !apart(in[i]->ptr, nb, a->q_out.ptr, rows_bytes(a->q_out, plan->Hq, d)))
+            return LITE_ERR_INVALID_ARG;
+    }
+    if (has_q) {
+        const size_t nb = rows_bytes(a->q_out, plan->Hq, d);
+        if (!apart(a->q_out.ptr, nb, c.k, cb) || !apart(a->q_out.ptr, nb, c.v, cb)) return LITE_ERR_INVALID_ARG;
+    }
+    if (fault("launch")) return LITE_ERR_CUDA;
+    NvtxRange range("lite_attn_cache_append");
+
+    AppendParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = static_cast<const uint16_t *>(a->q.ptr), p.k = static_cast<const uint16_t *>(a->k.ptr);
+    p.v = static_cast<const uint16_t *>(a->v.ptr), p.q_out = static_cast<uint16_t *>(a->q_out.ptr);
+    p.kc = static_cast<uint16_t *>(a->k_pages), p.vc = static_cast<uint16_t *>(a->v_pages);
+    p.q_st = a->q.stride_token, p.q_sh = a->q.stride_head, p.k_st = a->k.stride_token, p.k_sh = a->k.stride_head;
+    p.v_st = a->v.stride_token, p.v_sh = a->v.stride_head, p.qo_st = a->q_out.stride_token, p.qo_sh = a->q_out.stride_head;
+    p.c_sp = static_cast<int64_t>(a->page) * plan->Hk * d;
+    p.c_sh = a->layout == LITE_LAYOUT_BHND ? static_cast<int64_t>(a->page) * d : d;
+    p.c_st = a->layout == LITE_LAYOUT_BHND ? d : static_cast<int64_t>(plan->Hk) * d;
+    p.cos = a->cos, p.sin = a->sin, p.positions = a->positions, p.n_pos = a->angle_rows;
+    p.Hq = plan->Hq, p.Hk = plan->Hk, p.D = d, p.rot = a->cos ? a->rot : 0, p.interleaved = a->interleaved ? 1 : 0;
+    p.has_q = has_q ? 1 : 0;
+    p.b.cu_q = a->cu_new, p.b.lens = a->lens, p.b.table = a->table, p.b.Tq = a->k.tokens, p.b.pages = a->pages;
+    p.b.max_keys = static_cast<int64_t>(a->table_width) * a->page, p.b.status = plan->status, p.b.B = a->B;
+    p.b.mode = a->layout == LITE_LAYOUT_BHND ? kKvPagesBhnd : kKvPagesBnhd;
+    p.b.table_w = a->table_width, p.b.page_shift = log2_page(a->page);
+    // One token per block while the tokens do not fill the GPU twice over; several then.
+    const int slots = kAppendThreads / (d / 16);
+    const int heads = (has_q ? plan->Hq : 0) + 2 * plan->Hk;
+    int lanes = slots;
+    while (lanes > 1 && lanes / 2 >= heads) lanes /= 2;      // no lane without a head
+    while (lanes > 4 && a->k.tokens * lanes / slots > 4 * plan->sms) lanes /= 2;
+    p.head_lanes = lanes;
+    p.tokens_per_block = slots / lanes;
+    const int64_t blocks = (a->k.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (plan->dtype == LITE_DTYPE_FP16) rope_append_kernel<true><<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p);
+    else rope_append_kernel<false><<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p);
+    g_launches.fetch_add(1);
+    return cuda_err(cudaGetLastError());
+}
+
+int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *a, void *stream) {
+    if (!valid_gqa(plan) || !a || a->B < 0 || a->table_width < 1 || a->max_new < 0)
+        return LITE_ERR_INVALID_ARG;
+    if (!(a->scale > 0.0f) || std::isinf(a->scale) || a->q.tokens != a->o.tokens) return LITE_ERR_INVALID_ARG;
+    const int dev = plan->device, d = plan->d;
+    const CacheView c{a->k_pages, a->v_pages, a->pages, a->page, a->layout};
+    DeviceScope ds(dev);
+    if (!ds.ok) return LITE_ERR_CUDA;
+    int rc = check_cache(plan, c);
+    if (rc != LITE_OK) return rc;
+    if (a->q.tokens == 0 || a->B == 0) return LITE_OK;
+    if (a->q.tokens * plan->Hq >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(a->table_width) * a->page >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
+    if (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->o, plan->Hq, d, dev)) return LITE_ERR_INVALID_ARG;
+    if (!ints_ok(a->cu_new, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->lens, a->B, dev) ||
+        !ints_ok(a->table, static_cast<size_t>(a->B) * a->table_width, dev))
+        return LITE_ERR_INVALID_ARG;
+    const size_t ob = rows_bytes(a->o, plan->Hq, d), cb = cache_bytes(plan, c);
+    if (!apart(a->o.ptr, ob, a->q.ptr, rows_bytes(a->q, plan->Hq, d)) || !apart(a->o.ptr, ob, c.k, cb) ||
+        !apart(a->o.ptr, ob, c.v, cb))
+        return LITE_ERR_INVALID_ARG;
+    NvtxRange range("lite_attn_cache_attend");
+    GqaBatch b;
+    std::memset(&b, 0, sizeof b);
+    b.cu_q = a->cu_new, b.lens = a->lens, b.table = a->table, b.Tq = a->q.tokens, b.pages = a->pages;
+    b.max_keys = static_cast<int64_t>(a->table_width) * a->page, b.B = a->B, b.causal = a->causal ? 1 : 0;
+    b.mode = a->layout == LITE_LAYOUT_BHND ? kKvPagesBhnd : kKvPagesBnhd;
+    b.table_w = a->table_width, b.page_shift = log2_page(a->page);
+    return attention(plan, &c, nullptr, nullptr, a->q, a->o, b, a->scale, a->workspace, a->workspace_bytes,
+                     static_cast<cudaStream_t>(stream));
+}
+
+int lite_attn_prompt(lite_attn_gqa_t plan, const lite_attn_prompt_t *a, void *stream) {
+    if (!valid_gqa(plan) || !a || a->B < 0) return LITE_ERR_INVALID_ARG;
+    if (!(a->scale > 0.0f) || std::isinf(a->scale) || a->q.tokens != a->o.tokens || a->k.tokens != a->v.tokens)
+        return LITE_ERR_INVALID_ARG;
+    const int dev = plan->device, d = plan->d;
+    DeviceScope ds(dev);
+    if (!ds.ok) return LITE_ERR_CUDA;
+    if (a->q.tokens == 0 || a->B == 0) return LITE_OK;
+    if (a->q.tokens * plan->Hq >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
+    if (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->o, plan->Hq, d, dev) || !rows_ok(a->k, plan->Hk, d, dev) ||
+        !rows_ok(a->v, plan->Hk, d, dev))
+        return LITE_ERR_INVALID_ARG;
+    if (!ints_ok(a->cu_q, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->cu_k, static_cast<size_t>(a->B) + 1, dev))
+        return LITE_ERR_INVALID_ARG;
+    const size_t ob = rows_bytes(a->o, plan->Hq, d);
+    if (!apart(a->o.ptr, ob, a->q.ptr, rows_bytes(a->q, plan->Hq, d)) || !apart(a->o.ptr, ob, a->k.ptr, rows_bytes(a->k, plan->Hk, d)) ||
+        !apart(a->o.ptr, ob, a->v.ptr, rows_bytes(a->v, plan->Hk, d)))
+        return LITE_ERR_INVALID_ARG;
+    NvtxRange range("lite_attn_prompt");
+    GqaBatch b;
+    std::memset(&b, 0, sizeof b);
+    b.cu_q = a->cu_q, b.cu_k = a->cu_k, b.Tq = a->q.tokens, b.Tk = a->k.tokens, b.pages = 1;
+    b.B = a->B, b.causal = a->causal ? 1 : 0, b.mode = kKvPacked;
+    return attention(plan, nullptr, &a->k, &a->v, a->q, a->o, b, a->scale, a->workspace, a->workspace_bytes,
+                     static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

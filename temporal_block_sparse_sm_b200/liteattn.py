@@ -34,6 +34,8 @@ LITE_LAYOUT_BHND = 0   # q, k, v, o as [B][H][N][d]
 LITE_LAYOUT_BNHD = 1   # q, k, v, o as [B][N][H][d]
 LITE_PRED_THRESHOLD = 0   # QK-Skip against a per-step threshold
 LITE_PRED_RECALL = 1      # fixed recall p per step
+LITE_DTYPE_BF16 = 0
+LITE_DTYPE_FP16 = 1
 _LAYOUTS = {"bhnd": LITE_LAYOUT_BHND, "bnhd": LITE_LAYOUT_BNHD}
 
 
@@ -59,6 +61,37 @@ class Stats(ctypes.Structure):
 _lib = None
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
+_I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+
+
+class Rows(ctypes.Structure):
+    """lite_attn_rows_t."""
+    _fields_ = [("ptr", _VP), ("tokens", _I64), ("stride_token", _I64), ("stride_head", _I64)]
+
+
+class AppendArgs(ctypes.Structure):
+    """lite_attn_append_t."""
+    _fields_ = [("q", Rows), ("q_out", Rows), ("k", Rows), ("v", Rows), ("k_pages", _VP), ("v_pages", _VP),
+                ("pages", _I64), ("cos", _VP), ("sin", _VP), ("angle_rows", _I64), ("positions", _VP), ("cu_new", _VP),
+                ("lens", _VP), ("table", _VP), ("B", _I32), ("table_width", _I32), ("page", _I32), ("layout", _I32),
+                ("rot", _I32), ("interleaved", _I32)]
+
+
+class AttendArgs(ctypes.Structure):
+    """lite_attn_attend_t."""
+    _fields_ = [("q", Rows), ("o", Rows), ("k_pages", _VP), ("v_pages", _VP), ("pages", _I64), ("cu_new", _VP),
+                ("lens", _VP), ("table", _VP), ("workspace", _VP), ("workspace_bytes", ctypes.c_size_t), ("B", _I32),
+                ("table_width", _I32), ("page", _I32), ("layout", _I32), ("max_new", _I32), ("causal", _I32),
+                ("scale", ctypes.c_float), ("reserved", _I32)]
+
+
+class PromptArgs(ctypes.Structure):
+    """lite_attn_prompt_t."""
+    _fields_ = [("q", Rows), ("o", Rows), ("k", Rows), ("v", Rows), ("cu_q", _VP), ("cu_k", _VP), ("workspace", _VP),
+                ("workspace_bytes", ctypes.c_size_t), ("B", _I32), ("causal", _I32), ("scale", ctypes.c_float),
+                ("reserved", _I32)]
+
 
 # name -> (restype, argtypes): the exported symbols of include/liteattn.h
 SIGNATURES = {
@@ -90,6 +123,13 @@ SIGNATURES = {
     "lite_attn_timing_read": (_I, [_VP, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double),
                                    ctypes.POINTER(ctypes.c_int64)]),
     "lite_attn_compact_noalloc": (_I, [_VP, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP]),
+    "lite_attn_gqa_create": (_I, [ctypes.POINTER(_VP), _I, _I, _I, _I]),
+    "lite_attn_gqa_destroy": (_I, [_VP]),
+    "lite_attn_gqa_status": (_I, [_VP, _VP]),
+    "lite_attn_gqa_workspace": (_I, [_VP, _I, ctypes.c_int64, _I, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
+    "lite_attn_cache_append": (_I, [_VP, _VP, _VP]),
+    "lite_attn_cache_attend": (_I, [_VP, _VP, _VP]),
+    "lite_attn_prompt": (_I, [_VP, _VP, _VP]),
     "lite_attn_launch_count": (ctypes.c_int64, []),
     "lite_attn_error_string": (ctypes.c_char_p, [_I]),
 }
@@ -290,6 +330,42 @@ def lite_attn_compact_noalloc(bits_ptr: int, B: int, H: int, N: int, Br: int, Bc
     """Compaction into caller-owned device buffers; the library allocates nothing."""
     _check(load().lite_attn_compact_noalloc(bits_ptr, B, H, N, Br, Bc, list_ptr, cnt_ptr, order_ptr, live_total_ptr,
                                             _stream_ptr(stream)), "lite_attn_compact_noalloc")
+
+
+def lite_attn_gqa_create(Hq: int, Hk: int, d: int, dtype: int) -> int:
+    h = _VP()
+    _check(load().lite_attn_gqa_create(ctypes.byref(h), Hq, Hk, d, dtype), "lite_attn_gqa_create")
+    return h.value
+
+
+def lite_attn_gqa_destroy(plan: int):
+    _check(load().lite_attn_gqa_destroy(plan), "lite_attn_gqa_destroy")
+
+
+def lite_attn_gqa_status(plan: int, stream=None):
+    """Synchronises the stream; raises if a kernel of the plan reported an error."""
+    _check(load().lite_attn_gqa_status(plan, _stream_ptr(stream)), "lite_attn_gqa_status")
+
+
+def lite_attn_gqa_workspace(plan: int, B: int, tokens: int, max_new: int, max_keys: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().lite_attn_gqa_workspace(plan, B, tokens, max_new, max_keys, ctypes.byref(n)), "lite_attn_gqa_workspace")
+    return n.value
+
+
+def lite_attn_cache_append(plan: int, args, stream=None):
+    """args: an AppendArgs' address, or its bytes."""
+    _check(load().lite_attn_cache_append(plan, args, _stream_ptr(stream)), "lite_attn_cache_append")
+
+
+def lite_attn_cache_attend(plan: int, args, stream=None):
+    """args: an AttendArgs' address, or its bytes."""
+    _check(load().lite_attn_cache_attend(plan, args, _stream_ptr(stream)), "lite_attn_cache_attend")
+
+
+def lite_attn_prompt(plan: int, args, stream=None):
+    """args: a PromptArgs' address, or its bytes."""
+    _check(load().lite_attn_prompt(plan, args, _stream_ptr(stream)), "lite_attn_prompt")
 
 
 def lite_attn_launch_count() -> int:
