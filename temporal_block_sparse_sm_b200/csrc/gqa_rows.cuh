@@ -280,7 +280,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // weights, rounded to 16 bits for the product; the sum adds the rounded ones
             float neg[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) neg[r] = m_ref[r] == -INFINITY ? 0.0f : -m_ref[r] * cl2;
+            for (int r = 0; r < 2; ++r) neg[r] = (m_ref[r] == -INFINITY ? 0.0f : -m_ref[r] * cl2) + weight_bias<F16>();
             uint32_t pf[4];
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb)

@@ -12,6 +12,7 @@
 
 #include "liteattn.h"
 #include "gqa_rows.cuh"
+#include "gqa_tile.cuh"
 #include "host_util.cuh"
 #include "rope_append.cuh"
 #include "serving_internal.cuh"
@@ -124,27 +125,71 @@ int allow_smem(K kernel, std::atomic<bool> *done, int device, uint32_t bytes) {
     return LITE_OK;
 }
 
-// How a batch is divided among blocks: decided from what the host knows (tensor sizes).
+// q as a 4-D tensor map (d, head, row, 1); a box is the heads of a group by a slot's tokens.
+bool encode_q(CUtensorMap *m, const lite_attn_gqa *pl, const lite_attn_rows_t &q, int slot_tokens) {
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(pl->d), static_cast<cuuint64_t>(pl->Hq),
+                                static_cast<cuuint64_t>(q.tokens), 1};
+    const cuuint64_t strides[3] = {2u * static_cast<cuuint64_t>(q.stride_head), 2u * static_cast<cuuint64_t>(q.stride_token),
+                                   2u * static_cast<cuuint64_t>(q.stride_token) * dims[2]};
+    const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(pl->Hq / pl->Hk), static_cast<cuuint32_t>(slot_tokens), 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return driver().encode(m, pl->dtype == LITE_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           q.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a batch is divided among blocks: decided from what the host knows (tensor sizes and
+// the bounds that the caller gives), never from the lengths on the device.
 struct Division {
+    bool tile;            // the 256-row tcgen05 kernel, or the 16-row kernel
+    int rows;             // query rows of an item
     int64_t items;        // most work items there can be
     int target;           // split target, 0: no splitting
+    int min_tiles;        // shortest segment
     size_t workspace;
 };
 constexpr int kRowsMinTiles = 4;      // shortest segment, tiles of 64 keys
+constexpr int kTileMinTiles = 4;      // and of 128 keys
 
-Division divide_rows(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_keys) {
-    const int64_t G = pl->Hq / pl->Hk, rows = RowsCfg<128>::ROWS;
+Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_new, int64_t max_keys) {
+    const int64_t G = pl->Hq / pl->Hk;
+    max_new = std::min(max_new, tokens);
     Division dv;
-    dv.items = pl->Hk * std::min((tokens * G + B * (rows - 1)) / rows, tokens * G);
-    const int target = 2 * pl->sms;   // two blocks per SM
-    const int64_t least = pl->Hk * ((tokens * G + rows - 1) / rows);   // items of a batch without padding
-    dv.target = (least >= 2 * target || max_keys <= kRowsMinTiles * RowsCfg<128>::BN) ? 0 : target;
-    dv.workspace = dv.target ? static_cast<size_t>(2 * dv.target) * rows * (pl->d + 2) * 4u : 0;
+    dv.tile = max_new * G > RowsCfg<128>::ROWS;
+    int64_t least;        // items of a batch without padding
+    int64_t tile_keys;
+    if (dv.tile) {
+        const int64_t per = 2 * (128 / G);
+        dv.rows = 256;
+        dv.items = pl->Hk * std::min((tokens + B * (per - 1)) / per, tokens);
+        least = pl->Hk * ((tokens + per - 1) / per);
+        dv.target = pl->sms;          // one block per SM
+        dv.min_tiles = kTileMinTiles;
+        tile_keys = 128;
+    } else {
+        const int64_t rows = RowsCfg<128>::ROWS;
+        dv.rows = RowsCfg<128>::ROWS;
+        dv.items = pl->Hk * std::min((tokens * G + B * (rows - 1)) / rows, tokens * G);
+        least = pl->Hk * ((tokens * G + rows - 1) / rows);
+        dv.target = 2 * pl->sms;      // two blocks per SM
+        dv.min_tiles = kRowsMinTiles;
+        tile_keys = RowsCfg<128>::BN;
+    }
+    if (least >= 2 * dv.target || max_keys <= dv.min_tiles * tile_keys) dv.target = 0;
+    dv.workspace = static_cast<size_t>(2 * dv.target) * dv.rows * (pl->d + 2) * 4u;
     return dv;
 }
 
 template <int D, bool F16>
-int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMap &tv, GqaParams &p, const Division &dv,
+int launch_join(const GqaParams &p, const Division &dv, int slot_tokens, cudaStream_t s) {
+    if (!dv.target) return LITE_OK;
+    gqa_join_kernel<D, F16><<<dim3(static_cast<unsigned>(dv.items), dv.rows / 4), kJoinThreads, 0, s>>>(p, dv.rows, slot_tokens);
+    g_launches.fetch_add(1);
+    return cuda_err(cudaGetLastError());
+}
+
+template <int D, bool F16>
+int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMap &tv, const GqaParams &p, const Division &dv,
                 cudaStream_t s) {
     using C = RowsCfg<D>;
     static std::atomic<bool> done[kMaxDevices];
@@ -152,19 +197,38 @@ int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMa
     if (rc != LITE_OK) return rc;
     gqa_rows_kernel<D, F16><<<static_cast<unsigned>(dv.items + dv.target), C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
     g_launches.fetch_add(1);
-    if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target) return rc;
-    gqa_join_kernel<D, F16><<<dim3(static_cast<unsigned>(dv.items), C::ROWS / 4), kJoinThreads, 0, s>>>(p, C::ROWS, 0);
+    rc = cuda_err(cudaGetLastError());
+    return rc == LITE_OK ? launch_join<D, F16>(p, dv, 0, s) : rc;
+}
+
+template <int D, bool F16>
+int launch_tile(const lite_attn_gqa *pl, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                const TileParams &p, const Division &dv, cudaStream_t s) {
+    using C = TileCfg<D, F16>;
+    static std::atomic<bool> done[kMaxDevices];
+    if (pl->device < kMaxDevices && !done[pl->device].load(std::memory_order_acquire)) {
+        // the warpgroups' register split draws on what the block is launched with
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, gqa_tile_kernel<D, F16>) != cudaSuccess ||
+            attr.numRegs * C::NTHREADS < static_cast<int>(128 * C::REG_CTRL + 256 * C::REG_SOFTMAX)) {
+            cudaGetLastError();
+            return LITE_ERR_CUDA;
+        }
+    }
+    int rc = allow_smem(gqa_tile_kernel<D, F16>, done, pl->device, C::SMEM_BYTES);
+    if (rc != LITE_OK) return rc;
+    gqa_tile_kernel<D, F16><<<static_cast<unsigned>(dv.items + dv.target), C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
     g_launches.fetch_add(1);
-    return cuda_err(cudaGetLastError());
+    rc = cuda_err(cudaGetLastError());
+    return rc == LITE_OK ? launch_join<D, F16>(p.a, dv, p.slot_tokens, s) : rc;
 }
 
 // Attention of q over the cache (c) or packed rows (k, v).
 int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, const lite_attn_rows_t *v,
-              const lite_attn_rows_t &q, const lite_attn_rows_t &o, GqaBatch b, float scale, void *workspace,
-              size_t workspace_bytes, cudaStream_t s) {
+              const lite_attn_rows_t &q, const lite_attn_rows_t &o, GqaBatch b, int64_t max_new, float scale,
+              void *workspace, size_t workspace_bytes, cudaStream_t s) {
     const int G = pl->Hq / pl->Hk;
-    const int64_t max_keys = c ? b.max_keys : b.Tk;
-    const Division dv = divide_rows(pl, b.B, q.tokens, max_keys);
+    const Division dv = divide(pl, b.B, q.tokens, max_new, c ? b.max_keys : b.Tk);
     if (dv.items + dv.target >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
     if (workspace_bytes < dv.workspace) return LITE_ERR_INVALID_ARG;
     if (dv.workspace && !device_range_ok(workspace, dv.workspace, pl->device)) return LITE_ERR_INVALID_ARG;
@@ -173,33 +237,48 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     b.G = G;
     b.Hk = pl->Hk;
     b.status = pl->status;
-    b.unit_rows = RowsCfg<128>::ROWS;
-    b.unit_tokens = 0;
-    b.tile = RowsCfg<128>::BN;
+    b.unit_rows = dv.tile ? 0 : dv.rows;
+    b.unit_tokens = dv.tile ? 2 * (128 / G) : 0;
+    b.tile = dv.tile ? 128 : RowsCfg<128>::BN;
     b.split_target = dv.target;
-    b.min_tiles = kRowsMinTiles;
-    GqaParams p;
+    b.min_tiles = dv.min_tiles;
+    TileParams t;
+    std::memset(&t, 0, sizeof t);
+    GqaParams &p = t.a;
     p.b = b;
     p.q = static_cast<const uint16_t *>(q.ptr);
     p.o = static_cast<uint16_t *>(o.ptr);
     p.q_st = q.stride_token, p.q_sh = q.stride_head, p.o_st = o.stride_token, p.o_sh = o.stride_head;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.ws_ml = static_cast<float *>(workspace);
-    p.ws_o = p.ws_ml + static_cast<size_t>(2 * dv.target) * b.unit_rows * 2;
+    p.ws_o = p.ws_ml + static_cast<size_t>(2 * dv.target) * dv.rows * 2;
     const int box = c ? std::min(c->page, b.tile) : b.tile;
-    CUtensorMap tk, tv;
+    CUtensorMap tq, tk, tv;
+    std::memset(&tq, 0, sizeof tq);
     std::memset(&tk, 0, sizeof tk);
     std::memset(&tv, 0, sizeof tv);
     if (c) {
         CacheView cv = *c;
         cv.k = c->v;
         if (!encode_kv(&tk, pl, c, nullptr, box) || !encode_kv(&tv, pl, &cv, nullptr, box)) return LITE_ERR_CUDA;
+        t.v = static_cast<const uint16_t *>(c->v);
+        t.v_page = static_cast<int64_t>(c->page) * pl->Hk * pl->d;
+        t.v_head = c->layout == LITE_LAYOUT_BHND ? static_cast<int64_t>(c->page) * pl->d : pl->d;
+        t.v_token = c->layout == LITE_LAYOUT_BHND ? pl->d : static_cast<int64_t>(pl->Hk) * pl->d;
     } else if (k->tokens > 0) {   // without keys nothing is loaded
         if (!encode_kv(&tk, pl, nullptr, k, box) || !encode_kv(&tv, pl, nullptr, v, box)) return LITE_ERR_CUDA;
+        t.v = static_cast<const uint16_t *>(v->ptr);
+        t.v_token = v->stride_token, t.v_head = v->stride_head;
     }
     const bool f16 = pl->dtype == LITE_DTYPE_FP16;
-    if (pl->d == 64) return f16 ? launch_rows<64, true>(pl, tk, tv, p, dv, s) : launch_rows<64, false>(pl, tk, tv, p, dv, s);
-    return f16 ? launch_rows<128, true>(pl, tk, tv, p, dv, s) : launch_rows<128, false>(pl, tk, tv, p, dv, s);
+    if (!dv.tile) {
+        if (pl->d == 64) return f16 ? launch_rows<64, true>(pl, tk, tv, p, dv, s) : launch_rows<64, false>(pl, tk, tv, p, dv, s);
+        return f16 ? launch_rows<128, true>(pl, tk, tv, p, dv, s) : launch_rows<128, false>(pl, tk, tv, p, dv, s);
+    }
+    t.slot_tokens = 128 / G;
+    if (!encode_q(&tq, pl, q, t.slot_tokens)) return LITE_ERR_CUDA;
+    if (pl->d == 64) return f16 ? launch_tile<64, true>(pl, tq, tk, tv, t, dv, s) : launch_tile<64, false>(pl, tq, tk, tv, t, dv, s);
+    return f16 ? launch_tile<128, true>(pl, tq, tk, tv, t, dv, s) : launch_tile<128, false>(pl, tq, tk, tv, t, dv, s);
 }
 
 }  // namespace
@@ -264,7 +343,7 @@ int lite_attn_gqa_status(lite_attn_gqa_t plan, void *stream) {
 
 int lite_attn_gqa_workspace(lite_attn_gqa_t plan, int B, int64_t tokens, int max_new, int64_t max_keys, size_t *bytes) {
     if (!valid_gqa(plan) || !bytes || B < 0 || tokens < 0 || max_new < 0 || max_keys < 0) return LITE_ERR_INVALID_ARG;
-    *bytes = divide_rows(plan, B, tokens, max_keys).workspace;
+    *bytes = divide(plan, B, tokens, max_new, max_keys).workspace;
     return LITE_OK;
 }
 
@@ -374,7 +453,7 @@ int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *a, vo
     b.max_keys = static_cast<int64_t>(a->table_width) * a->page, b.B = a->B, b.causal = a->causal ? 1 : 0;
     b.mode = a->layout == LITE_LAYOUT_BHND ? kKvPagesBhnd : kKvPagesBnhd;
     b.table_w = a->table_width, b.page_shift = log2_page(a->page);
-    return attention(plan, &c, nullptr, nullptr, a->q, a->o, b, a->scale, a->workspace, a->workspace_bytes,
+    return attention(plan, &c, nullptr, nullptr, a->q, a->o, b, a->max_new, a->scale, a->workspace, a->workspace_bytes,
                      static_cast<cudaStream_t>(stream));
 }
 
@@ -401,7 +480,7 @@ int lite_attn_prompt(lite_attn_gqa_t plan, const lite_attn_prompt_t *a, void *st
     std::memset(&b, 0, sizeof b);
     b.cu_q = a->cu_q, b.cu_k = a->cu_k, b.Tq = a->q.tokens, b.Tk = a->k.tokens, b.pages = 1;
     b.B = a->B, b.causal = a->causal ? 1 : 0, b.mode = kKvPacked;
-    return attention(plan, nullptr, &a->k, &a->v, a->q, a->o, b, a->scale, a->workspace, a->workspace_bytes,
+    return attention(plan, nullptr, &a->k, &a->v, a->q, a->o, b, a->q.tokens, a->scale, a->workspace, a->workspace_bytes,
                      static_cast<cudaStream_t>(stream));
 }
 
