@@ -23,7 +23,6 @@
 // with scalar code that leaves hidden keys out.
 #pragma once
 
-#include "attn_kernel.cuh"   // WaitCtx, wait_bar, drain_wait
 #include "serving_internal.cuh"
 
 namespace lite {
@@ -159,7 +158,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int t_end = (lim_hi + BN - 1) / BN;
     const int t_hi = w.L >= t_end - t_lo ? t_end : t_lo + w.L;   // t_hi <= t_lo: an empty segment
     if (t_hi <= t_lo && w.segs > 1) return;                      // the join does not read it
-    const WaitCtx wctx{&s_abort, p.b.status};
+    const WaitScope wctx{&s_abort, p.b.status};
 
     if (warp == C::NWARP) {
         // ------------------------------------------------------------ loads
@@ -169,7 +168,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int t = t_lo; t < t_hi; ++t) {
             const int e = t - t_lo, st = e % NST;
             const int next = t + 1 < t_hi ? kv.page_of(t + 1, lane) : -1;
-            if (!__all_sync(0xFFFFFFFFu, wait_bar(empty(st), ((e / NST) & 1) ^ 1u, wctx))) break;
+            if (!wait_phase_warp(empty(st), ((e / NST) & 1) ^ 1u, wctx)) break;
             if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), kv.boxes(t) * kv.box * D * 4u);
             __syncwarp();
             const uint32_t dst = base_s + st * 2u * C::KV_BYTES;
@@ -180,7 +179,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             issued = t + 1;
         }
         // every copy that this block started lands before it exits
-        for (int e = max(0, issued - t_lo - NST); e < issued - t_lo; ++e) drain_wait(full(e % NST), (e / NST) & 1);
+        for (int e = max(0, issued - t_lo - NST); e < issued - t_lo; ++e) drain_phase(full(e % NST), (e / NST) & 1);
         return;
     }
 
@@ -214,7 +213,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int mi = lane >> 3, mr = lane & 7;
     for (int t = t_lo; t < t_hi; ++t) {
         const int e = t - t_lo, st = e % NST;
-        const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(full(st), (e / NST) & 1, wctx));
+        const bool ok = wait_phase_warp(full(st), (e / NST) & 1, wctx);
         const int kb = t * BN + warp * 16;             // the warp's first key
         if (ok && kb < lim_hi) {
             const uint32_t kt = base_s + st * 2u * C::KV_BYTES, vt = kt + C::KV_BYTES;
@@ -402,46 +401,23 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
 }
 
-// Joins the segments of split items: a warp per row, over the item's segments
+// Joins the parts of a row, one warp: `part(s)` is the workspace row of part s.
 //   o = sum_s 2^(c (m_s - m)) O_s / sum_s 2^(c (m_s - m)) l_s.
-// Grid: (items, row groups of four).  Items of one segment have written their output.
 constexpr int kJoinThreads = 128;
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams p, int rows_per_item, int slot_tokens) {
-    __shared__ ScanScratch scan;
-    WorkItem w;
-    if (!find_work<kJoinThreads, false>(p.b, blockIdx.x, scan, w) || w.segs <= 1) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.y * (kJoinThreads / 32) + warp, G = p.b.G;
-    // the item's rows: flattened (token, head), or per slot of slot_tokens tokens in 128 rows
-    int t, g, t_last;
-    if (p.b.unit_rows) {
-        const int r = w.i * p.b.unit_rows + row;
-        t = r / G, g = r % G;
-        t_last = static_cast<int>((min(static_cast<int64_t>(w.i + 1) * p.b.unit_rows, static_cast<int64_t>(w.s.n) * G) - 1) / G);
-        if (row >= p.b.unit_rows) return;
-    } else {
-        const int r = row & 127;
-        if (r >= slot_tokens * G) return;
-        t = w.i * p.b.unit_tokens + (row >> 7) * slot_tokens + r / G, g = r % G;
-        t_last = min((w.i + 1) * p.b.unit_tokens, w.s.n) - 1;
-    }
-    if (t >= w.s.n) return;
-    const int vis = visible_keys(p.b, w.s, t);
-    const int t_end = (visible_keys(p.b, w.s, t_last) + p.b.tile - 1) / p.b.tile;
-    const int segs = t_end > 0 ? (t_end + w.L - 1) / w.L : 0;     // segments that were written
-    const int64_t first = static_cast<int64_t>(w.slot) * rows_per_item + row;
+template <int D, bool F16, typename Part>
+__device__ __forceinline__ void join_row(const GqaParams &p, int parts, Part part, bool empty, uint16_t *o) {
+    const int lane = threadIdx.x & 31;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
     float mx = -INFINITY;
-    for (int s = lane; s < segs; s += 32) mx = fmaxf(mx, ml[first + static_cast<int64_t>(s) * rows_per_item].x);
+    for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, ml[part(s)].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    for (int o2 = 16; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o2));
     constexpr int CPT = D / 32;
     float a[CPT] = {}, sum = 0.0f;
 #pragma unroll 4
-    for (int s = 0; s < segs; ++s) {
-        const int64_t at = first + static_cast<int64_t>(s) * rows_per_item;
+    for (int s = 0; s < parts; ++s) {
+        const int64_t at = part(s);
         const float2 x = ml[at];
         const float f = x.x == -INFINITY ? 0.0f : ptx::ex2((x.x - mx) * p.scale_log2);
         const float *src = p.ws_o + at * D + lane * CPT;
@@ -449,11 +425,29 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams 
         for (int c = 0; c < CPT; ++c) a[c] += f * src[c];
         sum += f * x.y;
     }
-    const float inv = vis == 0 ? 0.0f : 1.0f / sum;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st +
-                                                 (static_cast<int64_t>(w.h) * G + g) * p.o_sh + lane * CPT);
+    const float inv = empty ? 0.0f : 1.0f / sum;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(o + lane * CPT);
 #pragma unroll
     for (int c = 0; c < CPT / 2; ++c) dst[c] = pack16<F16>(a[2 * c] * inv, a[2 * c + 1] * inv);
+}
+
+// Split items of the rows kernel.  Grid: (items, 4 rows each).
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) gqa_rows_join_kernel(const GqaParams p) {
+    __shared__ ScanScratch scan;
+    WorkItem w;
+    if (!find_work<kJoinThreads, false>(p.b, blockIdx.x, scan, w) || w.segs <= 1) return;
+    constexpr int ROWS = RowsCfg<D>::ROWS;
+    const int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), G = p.b.G;
+    const int64_t r = static_cast<int64_t>(w.i) * ROWS + row, all = static_cast<int64_t>(w.s.n) * G;
+    if (r >= all) return;
+    const int t = static_cast<int>(r / G), g = static_cast<int>(r % G);
+    const int64_t last = min(static_cast<int64_t>(w.i + 1) * ROWS, all) - 1;
+    const int t_end = (visible_keys(p.b, w.s, static_cast<int>(last / G)) + p.b.tile - 1) / p.b.tile;
+    const int64_t first = static_cast<int64_t>(w.slot) * ROWS + row;
+    join_row<D, F16>(p, t_end > 0 ? (t_end + w.L - 1) / w.L : 0,   // the segments that were written
+                     [&](int s) { return first + static_cast<int64_t>(s) * ROWS; }, visible_keys(p.b, w.s, t) == 0,
+                     p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st + (static_cast<int64_t>(w.h) * G + g) * p.o_sh);
 }
 
 }  // namespace lite

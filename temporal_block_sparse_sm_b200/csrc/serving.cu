@@ -145,11 +145,9 @@ struct Division {
     int rows;             // query rows of an item
     int64_t items;        // most work items there can be
     int target;           // split target, 0: no splitting
-    int min_tiles;        // shortest segment
     size_t workspace;
 };
 constexpr int kRowsMinTiles = 4;      // shortest segment, tiles of 64 keys
-constexpr int kTileMinTiles = 4;      // and of 128 keys
 
 Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_new, int64_t max_keys) {
     const int64_t G = pl->Hq / pl->Hk;
@@ -157,35 +155,23 @@ Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_
     Division dv;
     dv.tile = max_new * G > RowsCfg<128>::ROWS;
     int64_t least;        // items of a batch without padding
-    int64_t tile_keys;
     if (dv.tile) {
         const int64_t per = 2 * (128 / G);
         dv.rows = 256;
         dv.items = pl->Hk * std::min((tokens + B * (per - 1)) / per, tokens);
         least = pl->Hk * ((tokens + per - 1) / per);
         dv.target = pl->sms;          // one block per SM
-        dv.min_tiles = kTileMinTiles;
-        tile_keys = 128;
+        if (least >= 8 * pl->sms || max_keys <= kJoinCost) dv.target = 0;   // whole items come out even, or splitting cannot pay
     } else {
         const int64_t rows = RowsCfg<128>::ROWS;
         dv.rows = RowsCfg<128>::ROWS;
         dv.items = pl->Hk * std::min((tokens * G + B * (rows - 1)) / rows, tokens * G);
         least = pl->Hk * ((tokens * G + rows - 1) / rows);
         dv.target = 2 * pl->sms;      // two blocks per SM
-        dv.min_tiles = kRowsMinTiles;
-        tile_keys = RowsCfg<128>::BN;
+        if (least >= 2 * dv.target || max_keys <= kRowsMinTiles * RowsCfg<128>::BN) dv.target = 0;
     }
-    if (least >= 2 * dv.target || max_keys <= dv.min_tiles * tile_keys) dv.target = 0;
     dv.workspace = static_cast<size_t>(2 * dv.target) * dv.rows * (pl->d + 2) * 4u;
     return dv;
-}
-
-template <int D, bool F16>
-int launch_join(const GqaParams &p, const Division &dv, int slot_tokens, cudaStream_t s) {
-    if (!dv.target) return LITE_OK;
-    gqa_join_kernel<D, F16><<<dim3(static_cast<unsigned>(dv.items), dv.rows / 4), kJoinThreads, 0, s>>>(p, dv.rows, slot_tokens);
-    g_launches.fetch_add(1);
-    return cuda_err(cudaGetLastError());
 }
 
 template <int D, bool F16>
@@ -197,8 +183,10 @@ int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMa
     if (rc != LITE_OK) return rc;
     gqa_rows_kernel<D, F16><<<static_cast<unsigned>(dv.items + dv.target), C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
     g_launches.fetch_add(1);
-    rc = cuda_err(cudaGetLastError());
-    return rc == LITE_OK ? launch_join<D, F16>(p, dv, 0, s) : rc;
+    if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target) return rc;
+    gqa_rows_join_kernel<D, F16><<<dim3(static_cast<unsigned>(dv.items), dv.rows / 4), kJoinThreads, 0, s>>>(p);
+    g_launches.fetch_add(1);
+    return cuda_err(cudaGetLastError());
 }
 
 template <int D, bool F16>
@@ -217,10 +205,14 @@ int launch_tile(const lite_attn_gqa *pl, const CUtensorMap &tq, const CUtensorMa
     }
     int rc = allow_smem(gqa_tile_kernel<D, F16>, done, pl->device, C::SMEM_BYTES);
     if (rc != LITE_OK) return rc;
-    gqa_tile_kernel<D, F16><<<static_cast<unsigned>(dv.items + dv.target), C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
+    // persistent blocks, one per SM; no more than there can be items, unless items may be cut
+    const unsigned grid = static_cast<unsigned>(dv.target ? pl->sms : std::min<int64_t>(dv.items, pl->sms));
+    gqa_tile_kernel<D, F16><<<grid, C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
     g_launches.fetch_add(1);
-    rc = cuda_err(cudaGetLastError());
-    return rc == LITE_OK ? launch_join<D, F16>(p.a, dv, p.slot_tokens, s) : rc;
+    if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target || grid < 2) return rc;
+    gqa_tile_join_kernel<D, F16><<<dim3(grid - 1, 256 / kTileJoinRows), kJoinThreads, 0, s>>>(p, static_cast<int>(grid));
+    g_launches.fetch_add(1);
+    return cuda_err(cudaGetLastError());
 }
 
 // Attention of q over the cache (c) or packed rows (k, v).
@@ -241,7 +233,7 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     b.unit_tokens = dv.tile ? 2 * (128 / G) : 0;
     b.tile = dv.tile ? 128 : RowsCfg<128>::BN;
     b.split_target = dv.target;
-    b.min_tiles = dv.min_tiles;
+    b.min_tiles = kRowsMinTiles;
     TileParams t;
     std::memset(&t, 0, sizeof t);
     GqaParams &p = t.a;
