@@ -120,6 +120,8 @@ struct KvTiles {
     }
 };
 
+__device__ __forceinline__ void join_may_start();
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(RowsCfg<D>::NTHREADS, 2)
 gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
@@ -149,6 +151,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     WorkItem w;
     const bool any = find_work<C::NTHREADS, true>(p.b, blockIdx.x, scan, w);
     __syncthreads();
+    join_may_start();
     if (!any) return;
 
     const int G = p.b.G;
@@ -401,22 +404,30 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
 }
 
-// Joins the parts of a row, one warp: `part(s)` is the workspace row of part s.
-//   o = sum_s 2^(c (m_s - m)) O_s / sum_s 2^(c (m_s - m)) l_s.
+// The join may be launched while the kernel that writes the parts still runs: it looks up its
+// work first and waits for the parts then.
+__device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr int kJoinThreads = 128;
 
-template <int D, bool F16, typename Part>
-__device__ __forceinline__ void join_row(const GqaParams &p, int parts, Part part, bool empty, uint16_t *o) {
+// Joins the parts of a row:  o = sum_s 2^(c (m_s - m)) O_s / sum_s 2^(c (m_s - m)) l_s.
+// Warp `w` of `warps` takes every warps-th part; part(s) is the workspace row of part s.  Returns
+// the sums of the warp's share in the frame of the row's maximum m.
+template <int D, typename Part>
+__device__ __forceinline__ void join_share(const GqaParams &p, int parts, Part part, int w, int warps, float (&a)[D / 32], float &sum) {
     const int lane = threadIdx.x & 31;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
     float mx = -INFINITY;
     for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, ml[part(s)].x);
 #pragma unroll
-    for (int o2 = 16; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o2));
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
     constexpr int CPT = D / 32;
-    float a[CPT] = {}, sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) a[c] = 0.0f;
+    sum = 0.0f;
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
+    for (int s = w; s < parts; s += warps) {
         const int64_t at = part(s);
         const float2 x = ml[at];
         const float f = x.x == -INFINITY ? 0.0f : ptx::ex2((x.x - mx) * p.scale_log2);
@@ -425,29 +436,48 @@ __device__ __forceinline__ void join_row(const GqaParams &p, int parts, Part par
         for (int c = 0; c < CPT; ++c) a[c] += f * src[c];
         sum += f * x.y;
     }
+}
+template <int D, bool F16>
+__device__ __forceinline__ void write_row(uint16_t *o, const float (&a)[D / 32], float sum, bool empty) {
     const float inv = empty ? 0.0f : 1.0f / sum;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(o + lane * CPT);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(o + (threadIdx.x & 31) * (D / 32));
 #pragma unroll
-    for (int c = 0; c < CPT / 2; ++c) dst[c] = pack16<F16>(a[2 * c] * inv, a[2 * c + 1] * inv);
+    for (int c = 0; c < D / 64; ++c) dst[c] = pack16<F16>(a[2 * c] * inv, a[2 * c + 1] * inv);
 }
 
-// Split items of the rows kernel.  Grid: (items, 4 rows each).
+// Split items of the rows kernel, a block per row: the parts (up to a hundred and more) are
+// shared among its warps.  Grid: (items, rows of an item).
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) gqa_rows_join_kernel(const GqaParams p) {
+    constexpr int ROWS = RowsCfg<D>::ROWS, WARPS = kJoinThreads / 32, CPT = D / 32;
     __shared__ ScanScratch scan;
+    __shared__ float s_a[WARPS][32][CPT + 1];
     WorkItem w;
     if (!find_work<kJoinThreads, false>(p.b, blockIdx.x, scan, w) || w.segs <= 1) return;
-    constexpr int ROWS = RowsCfg<D>::ROWS;
-    const int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), G = p.b.G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y, G = p.b.G;
     const int64_t r = static_cast<int64_t>(w.i) * ROWS + row, all = static_cast<int64_t>(w.s.n) * G;
     if (r >= all) return;
     const int t = static_cast<int>(r / G), g = static_cast<int>(r % G);
     const int64_t last = min(static_cast<int64_t>(w.i + 1) * ROWS, all) - 1;
     const int t_end = (visible_keys(p.b, w.s, static_cast<int>(last / G)) + p.b.tile - 1) / p.b.tile;
     const int64_t first = static_cast<int64_t>(w.slot) * ROWS + row;
-    join_row<D, F16>(p, t_end > 0 ? (t_end + w.L - 1) / w.L : 0,   // the segments that were written
-                     [&](int s) { return first + static_cast<int64_t>(s) * ROWS; }, visible_keys(p.b, w.s, t) == 0,
-                     p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st + (static_cast<int64_t>(w.h) * G + g) * p.o_sh);
+    wait_for_parts();
+    float a[CPT], sum;
+    join_share<D>(p, t_end > 0 ? (t_end + w.L - 1) / w.L : 0,   // the segments that were written
+                  [&](int s) { return first + static_cast<int64_t>(s) * ROWS; }, warp, WARPS, a, sum);
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) s_a[warp][lane][c] = a[c];
+    s_a[warp][lane][CPT] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) {
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) a[c] += s_a[k][lane][c];
+        sum += s_a[k][lane][CPT];
+    }
+    write_row<D, F16>(p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st + (static_cast<int64_t>(w.h) * G + g) * p.o_sh, a, sum,
+                      visible_keys(p.b, w.s, t) == 0);
 }
 
 }  // namespace lite

@@ -36,8 +36,17 @@
 
 namespace lite {
 
+// What a block leaves for the join about the item that reaches beyond its stretch.
+struct JoinItem {
+    int parts, slot0;      // parts 0: there is none
+    int row0, tokens;      // rows of q and o of its first token; its tokens
+    int h, vis0;           // keys that the first token sees
+    int pad[2];
+};
+
 struct TileParams {
     GqaParams a;
+    JoinItem *joins;                    // workspace: [blocks]
     const uint16_t *v;                  // values in global memory (rows of values that are not finite)
     int64_t v_page, v_token, v_head;    // strides, elements (packed: v_token, v_head)
     int slot_tokens;                    // tokens of a slot: 128 / G
@@ -211,6 +220,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
     const GqaBatch &pb = p.a.b;
     const int64_t stretch = stretch_units<C::NTHREADS>(pb, gridDim.x, scan);
+    join_may_start();
     const WaitScope wctx{&s_abort, pb.status};
     if (warp == 2) {
         ptx::tmem_alloc(ptx::smem_u32(&s_tmem), C::TMEM_COLS);
@@ -228,6 +238,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // -------------------------------------------------------- work items
             WorkCursor cur;
             const bool line = stretch > 0;
+            if (p.joins && lane == 0) p.joins[blockIdx.x] = JoinItem{};
             cur.start(pb, line, lane);
             int64_t x = line ? blockIdx.x * stretch : 0;   // the next place on the line, or round of whole items
             const int64_t x_end = x + stretch;
@@ -248,6 +259,24 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         const bool mine = line_tiles(pb, it, stretch, blockIdx.x, t0, t1, whole);
                         slot = line_slot(it, stretch, blockIdx.x);
                         x = it.to;
+                        if (it.from >= blockIdx.x * stretch && it.to > x_end) {   // begins here, reaches beyond
+                            int parts = 0, slot0 = 0;
+                            bool all = false;
+                            // the stretches with tiles of the item are consecutive
+                            for (int64_t y = blockIdx.x; y * stretch < it.to && !all; ++y) {
+                                int c0, c1;
+                                if (!line_tiles(pb, it, stretch, y, c0, c1, all)) continue;
+                                if (parts++ == 0) slot0 = line_slot(it, stretch, y);
+                            }
+                            if (!all && lane == 0) {           // else one block writes it
+                                JoinItem *join = p.joins + blockIdx.x;
+                                join->parts = parts, join->slot0 = slot0;
+                                join->row0 = it.s.q0 + it.i * pb.unit_tokens;
+                                join->tokens = min(pb.unit_tokens, it.s.n - it.i * pb.unit_tokens);
+                                join->h = it.h;
+                                join->vis0 = pb.causal ? it.s.m - it.s.n + it.i * pb.unit_tokens + 1 : it.s.m;
+                            }
+                        }
                         if (mine) break;
                     } else {
                         const int grid = static_cast<int>(gridDim.x), blk = static_cast<int>(blockIdx.x);
@@ -769,61 +798,27 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (warp == 2) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// Items that lie across the end of a block's stretch.  Grid: (blocks of the tile kernel - 1,
-// 256 / kTileJoinRows); boundary x between stretch x and x + 1 joins the item that it is the
-// first to cut.  Finding the item takes a block longer than joining a row, hence several rows
-// per warp: with 4 rows a block the kernel took 82 us for the 147 boundaries, mostly searches.
-constexpr int kTileJoinRows = 32;
+// Items that lie across the end of a block's stretch, from what the blocks left about them.
+// Grid: (blocks of the tile kernel, 256 / kTileJoinRows), a warp per row at a time.  (Finding the
+// items again here took longer than joining them: 82 us for 147 of them, a block per 4 rows.)
+constexpr int kTileJoinRows = 16;
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) gqa_tile_join_kernel(const TileParams p, int blocks) {
-    __shared__ ScanScratch scan;
-    __shared__ LineItem s_item;
-    __shared__ int s_parts, s_slot0;
-    const GqaBatch &pb = p.a.b;
-    const int64_t stretch = stretch_units<kJoinThreads>(pb, blocks, scan);
-    if (stretch == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = pb.G;
-    if (warp == 0) {
-        const int64_t q = blockIdx.x, x = (q + 1) * stretch;   // the item begins in stretch q and reaches beyond x
-        int parts = 0, slot0 = 0;
-        WorkCursor cur;
-        cur.start(pb, true, lane);
-        LineItem it;
-        int b;
-        int64_t first;
-        if (cur.find(pb, true, lane, x, b, it.s, first)) {
-            line_item(pb, b, it.s, first, x, it);
-            if (it.from < x && it.from >= q * stretch) {
-                // the stretches with tiles of the item are consecutive
-                for (int64_t y = q; y * stretch < it.to; ++y) {
-                    int t0, t1;
-                    bool whole;
-                    if (!line_tiles(pb, it, stretch, y, t0, t1, whole)) continue;
-                    if (whole) {              // written by that block
-                        parts = 0;
-                        break;
-                    }
-                    if (parts == 0) slot0 = line_slot(it, stretch, y);
-                    ++parts;
-                }
-            }
-        }
-        if (lane == 0) s_item = it, s_parts = parts, s_slot0 = slot0;
-    }
-    __syncthreads();
-    const int parts = s_parts, slot0 = s_slot0;
-    if (parts == 0) return;
-    const LineItem &it = s_item;
-    for (int k = warp; k < kTileJoinRows; k += kJoinThreads / 32) {
+__global__ void __launch_bounds__(kJoinThreads) gqa_tile_join_kernel(const TileParams p) {
+    wait_for_parts();
+    const JoinItem it = p.joins[blockIdx.x];
+    if (it.parts == 0) return;
+    const int G = p.a.b.G;
+    for (int k = threadIdx.x >> 5; k < kTileJoinRows; k += kJoinThreads / 32) {
         const int row = blockIdx.y * kTileJoinRows + k;
         const int tl = (row & 127) / G, g = (row & 127) % G;
-        const int t = it.i * 2 * p.slot_tokens + (row >> 7) * p.slot_tokens + tl;
-        if (tl >= p.slot_tokens || t >= it.s.n) continue;
+        const int t = (row >> 7) * p.slot_tokens + tl;
+        if (tl >= p.slot_tokens || t >= it.tokens) continue;
+        float a[D / 32], sum;
         // the first part may sit in its block's second slot, the others in the first one of the blocks behind
-        join_row<D, F16>(p.a, parts, [&](int x) { return static_cast<int64_t>(x == 0 ? slot0 : (slot0 & ~1) + 2 * x) * 256 + row; },
-                         visible_keys(pb, it.s, t) == 0,
-                         p.a.o + (static_cast<int64_t>(it.s.q0) + t) * p.a.o_st + (static_cast<int64_t>(it.h) * G + g) * p.a.o_sh);
+        join_share<D>(p.a, it.parts, [&](int x) { return static_cast<int64_t>(x == 0 ? it.slot0 : (it.slot0 & ~1) + 2 * x) * 256 + row; }, 0, 1, a, sum);
+        write_row<D, F16>(p.a.o + (static_cast<int64_t>(it.row0) + t) * p.a.o_st + (static_cast<int64_t>(it.h) * G + g) * p.a.o_sh, a, sum,
+                          (p.a.b.causal ? it.vis0 + t : it.vis0) <= 0);
     }
 }
 

@@ -170,8 +170,27 @@ Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_
         dv.target = 2 * pl->sms;      // two blocks per SM
         if (least >= 2 * dv.target || max_keys <= kRowsMinTiles * RowsCfg<128>::BN) dv.target = 0;
     }
-    dv.workspace = static_cast<size_t>(2 * dv.target) * dv.rows * (pl->d + 2) * 4u;
+    dv.workspace = static_cast<size_t>(2 * dv.target) * dv.rows * (pl->d + 2) * 4u + static_cast<size_t>(dv.target) * sizeof(JoinItem);
     return dv;
+}
+
+// The kernel that joins split items, launched so that it may begin before the one in front of
+// it has ended (it waits for that one's results itself).
+template <typename K, typename P>
+int launch_join(K kernel, dim3 grid, const P &p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const int rc = cuda_err(cudaLaunchKernelEx(&cfg, kernel, p));
+    if (rc != LITE_OK) cudaGetLastError();
+    else g_launches.fetch_add(1);
+    return rc;
 }
 
 template <int D, bool F16>
@@ -184,9 +203,7 @@ int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMa
     gqa_rows_kernel<D, F16><<<static_cast<unsigned>(dv.items + dv.target), C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
     g_launches.fetch_add(1);
     if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target) return rc;
-    gqa_rows_join_kernel<D, F16><<<dim3(static_cast<unsigned>(dv.items), dv.rows / 4), kJoinThreads, 0, s>>>(p);
-    g_launches.fetch_add(1);
-    return cuda_err(cudaGetLastError());
+    return launch_join(gqa_rows_join_kernel<D, F16>, dim3(static_cast<unsigned>(dv.items), C::ROWS), p, s);
 }
 
 template <int D, bool F16>
@@ -210,9 +227,7 @@ int launch_tile(const lite_attn_gqa *pl, const CUtensorMap &tq, const CUtensorMa
     gqa_tile_kernel<D, F16><<<grid, C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
     g_launches.fetch_add(1);
     if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target || grid < 2) return rc;
-    gqa_tile_join_kernel<D, F16><<<dim3(grid - 1, 256 / kTileJoinRows), kJoinThreads, 0, s>>>(p, static_cast<int>(grid));
-    g_launches.fetch_add(1);
-    return cuda_err(cudaGetLastError());
+    return launch_join(gqa_tile_join_kernel<D, F16>, dim3(grid, 256 / kTileJoinRows), p, s);
 }
 
 // Attention of q over the cache (c) or packed rows (k, v).
@@ -244,6 +259,7 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.ws_ml = static_cast<float *>(workspace);
     p.ws_o = p.ws_ml + static_cast<size_t>(2 * dv.target) * dv.rows * 2;
+    t.joins = dv.target ? reinterpret_cast<JoinItem *>(p.ws_o + static_cast<size_t>(2 * dv.target) * dv.rows * pl->d) : nullptr;
     const int box = c ? std::min(c->page, b.tile) : b.tile;
     CUtensorMap tq, tk, tv;
     std::memset(&tq, 0, sizeof tq);

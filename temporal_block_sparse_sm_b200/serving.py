@@ -98,12 +98,13 @@ class GroupedPlan:
             n = self._ws[key] = _c.lite_attn_gqa_workspace(self.handle, B, tokens, max_new, max_keys)
         if not n:
             return None
-        # from the caching allocator, which reuses it in stream order (and keeps a captured graph's its own)
-        w = self._empty(n, dtype=self._u8, device=self._dev)
+        # from the caching allocator, on the call's own stream: reused in that stream's order, and a
+        # captured graph's workspace is the graph's own
         import torch
-        if stream != torch.cuda.current_stream(self.device).cuda_stream:
-            w.record_stream(torch.cuda.ExternalStream(stream, device=self._dev))
-        return w
+        if stream == torch.cuda.current_stream(self.device).cuda_stream:
+            return self._empty(n, dtype=self._u8, device=self._dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self._dev)):
+            return self._empty(n, dtype=self._u8, device=self._dev)
 
     def _scale(self, scale: Optional[float]) -> float:
         return 1.0 / math.sqrt(self.d) if scale is None else float(scale)
