@@ -11,11 +11,11 @@
 // below what even the legacy tensor path delivers, so nothing is gained from 128-row
 // tcgen05 tiles of which one row in eight would be used.
 //
-// A block is four computing warps and one that issues TMA loads of 64-key tiles into a ring
-// (three stages of 32 KB at D = 128; two blocks per SM keep up to 192 KB in flight).  A
-// computing warp owns 16 keys of every tile and keeps its own running maximum, sum and
-// output, so warps meet only at the ring's barriers; their states are joined once at the
-// end.
+// A block is four computing warps and one that walks the block's items and issues TMA loads of
+// 64-key tiles into a ring (three stages of 32 KB at D = 128; two blocks per SM keep up to
+// 192 KB in flight).  A computing warp owns 16 keys of every tile and keeps its own running
+// maximum, sum and output, so warps meet only at the ring's barriers; their states are joined at
+// an item's end, while the ring already fills with the next item's keys.
 //
 // Values that no row sees (behind the last key, in a page's unused part) are zeroed in
 // shared memory before the product, since 0 * NaN is NaN.  Where some rows see a key that
@@ -35,6 +35,7 @@ struct GqaParams {
     float scale_log2;                 // scale * log2 e
     float *ws_o;                      // workspace: [slot][rows of an item][D] unnormalised outputs
     float *ws_ml;                     // [slot][rows of an item][2]: running maximum (raw logit), sum
+    JoinItem *joins;                  // [blocks]; null: no item is cut
 };
 
 template <int D>
@@ -48,9 +49,7 @@ struct RowsCfg {
     static constexpr uint32_t CHUNK_BYTES = BN * 128u;
     static constexpr int NST = D == 128 ? 3 : 6;
     static constexpr uint32_t RING_BYTES = NST * 2u * KV_BYTES;
-    static constexpr int OSTRIDE = D + 4;       // floats, joins of the warps' outputs
     static constexpr uint32_t SMEM_BYTES = RING_BYTES + 1024u;
-    static_assert(NWARP * ROWS * OSTRIDE * 4u <= RING_BYTES, "join buffer");
 };
 
 namespace ptx {
@@ -87,10 +86,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, 
 template <int BN, int DCH>
 struct KvTiles {
     const GqaBatch &p;
-    const WorkItem &w;
-    int box;      // rows of a box
+    int64_t k0;   // first row of the sequence's keys (packed)
+    int b, h;     // sequence and key head
     int end;      // keys that any row of the item sees; boxes behind it are not loaded
-    __device__ __forceinline__ KvTiles(const GqaBatch &p_, const WorkItem &w_, int end_) : p(p_), w(w_), end(end_) {
+    int box;      // rows of a box
+    __device__ __forceinline__ KvTiles(const GqaBatch &p_, int64_t k0_, int b_, int h_, int end_) : p(p_), k0(k0_), b(b_), h(h_), end(end_) {
         const int page = p.mode == kKvPacked ? BN : 1 << p.page_shift;
         box = page < BN ? page : BN;
     }
@@ -102,7 +102,7 @@ struct KvTiles {
     __device__ __forceinline__ int page_of(int t, int lane) const {
         if (lane >= boxes(t)) return -1;
         if (p.mode == kKvPacked) return 0;
-        const int pg = __ldg(p.table + static_cast<int64_t>(w.b) * p.table_w + ((t * BN + lane * box) >> p.page_shift));
+        const int pg = __ldg(p.table + static_cast<int64_t>(b) * p.table_w + ((t * BN + lane * box) >> p.page_shift));
         if (pg >= 0 && pg < p.pages) return pg;
         atomicExch(p.status, kStatusCheck);
         return static_cast<int>(p.pages);   // outside the tensor map: reads as zeros
@@ -110,27 +110,38 @@ struct KvTiles {
     __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap *m, uint32_t bar, int t, int lane, int pg) const {
         if (pg < 0) return;
         const int j = t * BN + lane * box;
-        const int row = p.mode == kKvPacked ? static_cast<int>(w.s.k0) + j : j & ((1 << p.page_shift) - 1);
+        const int row = p.mode == kKvPacked ? static_cast<int>(k0) + j : j & ((1 << p.page_shift) - 1);
 #pragma unroll
         for (int c = 0; c < DCH; ++c) {
             const uint32_t at = dst + c * (BN * 128u) + static_cast<uint32_t>(lane * box) * 128u;
-            if (p.mode == kKvPagesBhnd) ptx::tma_load_4d(at, m, bar, c * 64, row, w.h, pg);
-            else ptx::tma_load_4d(at, m, bar, c * 64, w.h, row, pg);
+            if (p.mode == kKvPagesBhnd) ptx::tma_load_4d(at, m, bar, c * 64, row, h, pg);
+            else ptx::tma_load_4d(at, m, bar, c * 64, h, row, pg);
         }
     }
 };
 
-__device__ __forceinline__ void join_may_start();
+// The join may be launched while the kernel that writes the parts still runs, and waits for it.
+__device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// What the warps of a block need to know of one item (shared memory).
+struct RowsWork {
+    int q0, n, m, i, h;
+    int t0, t1, lim_lo, lim_hi;   // key tiles; keys that the first and the last row see
+    int whole, slot, valid;
+};
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(RowsCfg<D>::NTHREADS, 2)
 gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
     using C = RowsCfg<D>;
-    constexpr int BN = C::BN, NST = C::NST, DCH = C::DCH;
+    constexpr int BN = C::BN, NST = C::NST, DCH = C::DCH, NWORK = 2;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * NST];
+    __shared__ __align__(8) uint64_t bars[2 * NST + 2 * NWORK];
     __shared__ ScanScratch scan;
+    __shared__ RowsWork works[NWORK];
     __shared__ float s_ml[C::NWARP][C::ROWS][2];
+    __shared__ __align__(16) float s_o[C::NWARP][C::ROWS][36];   // 32 columns of the warps' outputs at a time
     __shared__ uint32_t s_abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,55 +150,85 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     uint8_t *base = smem_raw + (base_s - raw_s);
     auto full = [&](int st) { return ptx::smem_u32(bars + st); };
     auto empty = [&](int st) { return ptx::smem_u32(bars + NST + st); };
+    auto w_full = [&](int k) { return ptx::smem_u32(bars + 2 * NST + k); };
+    auto w_empty = [&](int k) { return ptx::smem_u32(bars + 2 * NST + NWORK + k); };
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < NST; ++st) {
             ptx::mbar_init(full(st), 1);
             ptx::mbar_init(empty(st), C::NWARP);
         }
+        for (int k = 0; k < NWORK; ++k) {
+            ptx::mbar_init(w_full(k), 1);
+            ptx::mbar_init(w_empty(k), C::NWARP);
+        }
         s_abort = 0u;
         ptx::fence_barrier_init();
     }
-    WorkItem w;
-    const bool any = find_work<C::NTHREADS, true>(p.b, blockIdx.x, scan, w);
+    const int64_t stretch = stretch_units<C::NTHREADS>(p.b, gridDim.x, scan);
     __syncthreads();
     join_may_start();
-    if (!any) return;
-
     const int G = p.b.G;
-    const int row0 = w.i * C::ROWS, nrows = min(C::ROWS, w.s.n * G - row0);
-    const int lim_lo = visible_keys(p.b, w.s, row0 / G), lim_hi = visible_keys(p.b, w.s, (row0 + nrows - 1) / G);
-    const int t_lo = w.seg * w.L;
-    const int t_end = (lim_hi + BN - 1) / BN;
-    const int t_hi = w.L >= t_end - t_lo ? t_end : t_lo + w.L;   // t_hi <= t_lo: an empty segment
-    if (t_hi <= t_lo && w.segs > 1) return;                      // the join does not read it
     const WaitScope wctx{&s_abort, p.b.status};
 
     if (warp == C::NWARP) {
-        // ------------------------------------------------------------ loads
-        KvTiles<BN, DCH> kv(p.b, w, lim_hi);
-        int pg = t_lo < t_hi ? kv.page_of(t_lo, lane) : -1;
-        int issued = t_lo;
-        for (int t = t_lo; t < t_hi; ++t) {
-            const int e = t - t_lo, st = e % NST;
-            const int next = t + 1 < t_hi ? kv.page_of(t + 1, lane) : -1;
-            if (!wait_phase_warp(empty(st), ((e / NST) & 1) ^ 1u, wctx)) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), kv.boxes(t) * kv.box * D * 4u);
+        // ------------------------------------------------------------ items and loads
+        BlockWalk walk;
+        walk.start(p.b, stretch, p.joins, lane);
+        int kv = 0;                  // tiles loaded so far
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const bool more = walk.next(p.b, p.joins, lane);
+            const LineItem &it = walk.it;
+            const int at = k % NWORK;
+            if (!wait_phase_warp(w_empty(at), ((k / NWORK) & 1) ^ 1u, wctx)) break;
+            if (lane == 0) {
+                RowsWork &w = works[at];
+                w.valid = more ? 1 : 0;
+                if (more) {
+                    w.q0 = it.s.q0, w.n = it.s.n, w.m = it.s.m, w.i = it.i, w.h = it.h, w.t0 = walk.t0, w.t1 = walk.t1;
+                    w.lim_lo = visible_keys(p.b, it.s, static_cast<int>(static_cast<int64_t>(it.i) * C::ROWS / G));
+                    w.lim_hi = it.keys, w.whole = walk.whole ? 1 : 0, w.slot = walk.slot;
+                }
+                ptx::mbar_arrive(w_full(at));
+            }
             __syncwarp();
-            const uint32_t dst = base_s + st * 2u * C::KV_BYTES;
-            kv.load(dst, &tm_k, full(st), t, lane, pg);
-            kv.load(dst + C::KV_BYTES, &tm_v, full(st), t, lane, pg);
-            __syncwarp();
-            pg = next;
-            issued = t + 1;
+            if (!more) break;
+            KvTiles<BN, DCH> tiles(p.b, it.s.k0, it.b, it.h, it.keys);
+            int pg = walk.t0 < walk.t1 ? tiles.page_of(walk.t0, lane) : -1;
+            for (int t = walk.t0; t < walk.t1; ++t, ++kv) {
+                const int st = kv % NST;
+                const int next = t + 1 < walk.t1 ? tiles.page_of(t + 1, lane) : -1;
+                if (!(ok = wait_phase_warp(empty(st), ((kv / NST) & 1) ^ 1u, wctx))) break;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), tiles.boxes(t) * tiles.box * D * 4u);
+                __syncwarp();
+                const uint32_t dst = base_s + st * 2u * C::KV_BYTES;
+                tiles.load(dst, &tm_k, full(st), t, lane, pg);
+                tiles.load(dst + C::KV_BYTES, &tm_v, full(st), t, lane, pg);
+                __syncwarp();
+                pg = next;
+            }
         }
         // every copy that this block started lands before it exits
-        for (int e = max(0, issued - t_lo - NST); e < issued - t_lo; ++e) drain_phase(full(e % NST), (e / NST) & 1);
+        for (int e = max(0, kv - NST); e < kv; ++e) drain_phase(full(e % NST), (e / NST) & 1);
         return;
     }
 
     // ---------------------------------------------------------------- computing warps
     const int gid = lane >> 2, tig = lane & 3;
+    const float cl2 = p.scale_log2;
+    const float resc = 8.0f / cl2;    // the reference moves when the maximum rose by over 2^8 in weight
+    int kv = 0;
+    for (int k = 0;; ++k) {
+    // one decision for the four warps, so that their barriers stay balanced
+    const bool known = wait_phase_warp(w_full(k % NWORK), (k / NWORK) & 1, wctx);
+    if (ptx::bar_red_or(1, 32 * C::NWARP, !known)) return;
+    const RowsWork w = works[k % NWORK];
+    if (!w.valid) return;
+    const SeqInfo seq{w.q0, w.n, w.m, 0};
+    const int64_t row0 = static_cast<int64_t>(w.i) * C::ROWS;
+    const int nrows = static_cast<int>(min(static_cast<int64_t>(C::ROWS), static_cast<int64_t>(w.n) * G - row0));
+    const int lim_lo = w.lim_lo, lim_hi = w.lim_hi;
     // the thread's two rows (of the item's 16): gid and gid + 8
     int lim[2];
     uint32_t qf[D / 16][4];
@@ -195,9 +236,9 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     for (int r = 0; r < 2; ++r) {
         const int row = gid + 8 * r;
         const bool ok = row < nrows;
-        const int t = ok ? (row0 + row) / G : 0, g = ok ? (row0 + row) % G : 0;
-        lim[r] = ok ? visible_keys(p.b, w.s, t) : 0;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (static_cast<int64_t>(w.s.q0) + t) * p.q_st +
+        const int t = ok ? static_cast<int>((row0 + row) / G) : 0, g = ok ? static_cast<int>((row0 + row) % G) : 0;
+        lim[r] = ok ? visible_keys(p.b, seq, t) : 0;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (static_cast<int64_t>(w.q0) + t) * p.q_st +
                                                                  (static_cast<int64_t>(w.h) * G + g) * p.q_sh);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -205,8 +246,6 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             qf[kk][2 + r] = ok ? __ldg(src + kk * 8 + 4 + tig) : 0u;
         }
     }
-    const float cl2 = p.scale_log2;
-    const float resc = 8.0f / cl2;    // the reference moves when the maximum rose by over 2^8 in weight
     float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     float acc[D / 8][4];
 #pragma unroll
@@ -214,9 +253,9 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
     // ldmatrix rows of this lane: matrix lane/8, row lane%8 of it
     const int mi = lane >> 3, mr = lane & 7;
-    for (int t = t_lo; t < t_hi; ++t) {
-        const int e = t - t_lo, st = e % NST;
-        const bool ok = wait_phase_warp(full(st), (e / NST) & 1, wctx);
+    for (int t = w.t0; t < w.t1; ++t, ++kv) {
+        const int st = kv % NST;
+        const bool ok = wait_phase_warp(full(st), (kv / NST) & 1, wctx);
         const int kb = t * BN + warp * 16;             // the warp's first key
         if (ok && kb < lim_hi) {
             const uint32_t kt = base_s + st * 2u * C::KV_BYTES, vt = kt + C::KV_BYTES;
@@ -343,71 +382,59 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             s_ml[warp][gid + 8 * r][1] = l[r];
         }
     }
-    ptx::bar_sync(1, 32 * C::NWARP);   // also: every warp has read its last tile, the ring is free
-    float *ob = reinterpret_cast<float *>(base);
+    ptx::bar_sync(1, 32 * C::NWARP);
     float f[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < C::NWARP; ++k) mx = fmaxf(mx, s_ml[k][gid + 8 * r][0]);
+        for (int j = 0; j < C::NWARP; ++j) mx = fmaxf(mx, s_ml[j][gid + 8 * r][0]);
         f[r] = m_ref[r] == -INFINITY ? 0.0f : ptx::ex2((m_ref[r] - mx) * cl2);
-        if (m_ref[r] != m_ref[r]) f[r] = m_ref[r];   // NaN logits stay NaN
     }
+    // 16 rows x 8 threads, four columns each of every 32
+    const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 4;
+    float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-        float *at = ob + (warp * C::ROWS + gid) * C::OSTRIDE + n * 8 + 2 * tig;
-        *reinterpret_cast<float2 *>(at) = make_float2(acc[n][0] * f[0], acc[n][1] * f[0]);
-        *reinterpret_cast<float2 *>(at + 8 * C::OSTRIDE) = make_float2(acc[n][2] * f[1], acc[n][3] * f[1]);
+    for (int j = 0; j < C::NWARP; ++j) mx = fmaxf(mx, s_ml[j][row][0]);
+#pragma unroll
+    for (int j = 0; j < C::NWARP; ++j) {
+        const float mj = s_ml[j][row][0];
+        sum += s_ml[j][row][1] * (mj == -INFINITY ? 0.0f : ptx::ex2((mj - mx) * cl2));   // 0 * NaN stays NaN
     }
-    ptx::bar_sync(1, 32 * C::NWARP);
-    constexpr int CPT = D / 8;          // columns per thread: 16 rows x 8 threads
-    const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * CPT;
-    if (row < nrows) {
-        float mx = -INFINITY, sum = 0.0f;
+    const int t = static_cast<int>((row0 + row) / G), g = static_cast<int>((row0 + row) % G);
+    // a row that sees no key is zero; one whose visible logits are all -inf is 0 / 0
+    const float inv = visible_keys(p.b, seq, t) == 0 ? 0.0f : 1.0f / sum;
+    uint16_t *dst = p.o + (static_cast<int64_t>(w.q0) + t) * p.o_st + (static_cast<int64_t>(w.h) * G + g) * p.o_sh + col;
+    const int64_t ws_at = static_cast<int64_t>(w.slot) * C::ROWS + row;
 #pragma unroll
-        for (int k = 0; k < C::NWARP; ++k) mx = fmaxf(mx, s_ml[k][row][0]);
+    for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
-        for (int k = 0; k < C::NWARP; ++k) {
-            const float mk = s_ml[k][row][0];
-            if (mk != -INFINITY) sum += s_ml[k][row][1] * ptx::ex2((mk - mx) * cl2);
+        for (int n = 0; n < 4; ++n) {
+            float *at = &s_o[warp][gid][n * 8 + 2 * tig];
+            const float (&a)[4] = acc[4 * c + n];
+            *reinterpret_cast<float2 *>(at) = make_float2(a[0] * f[0], a[1] * f[0]);
+            *reinterpret_cast<float2 *>(at + 8 * 36) = make_float2(a[2] * f[1], a[3] * f[1]);
         }
-        float v[CPT];
+        ptx::bar_sync(1, 32 * C::NWARP);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < CPT; c += 4) {
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < C::NWARP; ++k) {
-                const float4 b = *reinterpret_cast<const float4 *>(ob + (k * C::ROWS + row) * C::OSTRIDE + col + c);
-                a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-            }
-            v[c] = a.x, v[c + 1] = a.y, v[c + 2] = a.z, v[c + 3] = a.w;
+        for (int j = 0; j < C::NWARP; ++j) {
+            const float4 b = *reinterpret_cast<const float4 *>(&s_o[j][row][col]);
+            v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
         }
-        const int t = (row0 + row) / G, g = (row0 + row) % G;
-        if (w.segs == 1) {
-            // a row that sees no key is zero; one whose visible logits are all -inf is 0 / 0
-            const float inv = visible_keys(p.b, w.s, t) == 0 ? 0.0f : 1.0f / sum;
-            uint32_t pk[CPT / 2];
-#pragma unroll
-            for (int c = 0; c < CPT / 2; ++c) pk[c] = pack16<F16>(v[2 * c] * inv, v[2 * c + 1] * inv);
-            uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st +
-                                                   (static_cast<int64_t>(w.h) * G + g) * p.o_sh + col);
-#pragma unroll
-            for (int c = 0; c < CPT / 8; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        } else {
-            const int64_t at = static_cast<int64_t>(w.slot) * C::ROWS + row;
-            float4 *dst = reinterpret_cast<float4 *>(p.ws_o + at * D + col);
-#pragma unroll
-            for (int c = 0; c < CPT / 4; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            if ((threadIdx.x & 7) == 0) *reinterpret_cast<float2 *>(p.ws_ml + 2 * at) = make_float2(mx, sum);
+        if (row < nrows) {
+            if (w.whole)
+                *reinterpret_cast<uint2 *>(dst + 32 * c) = make_uint2(pack16<F16>(v.x * inv, v.y * inv), pack16<F16>(v.z * inv, v.w * inv));
+            else
+                *reinterpret_cast<float4 *>(p.ws_o + ws_at * D + 32 * c + col) = v;
         }
+        ptx::bar_sync(1, 32 * C::NWARP);
+    }
+    if (!w.whole && row < nrows && (threadIdx.x & 7) == 0) *reinterpret_cast<float2 *>(p.ws_ml + 2 * ws_at) = make_float2(mx, sum);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(w_empty(k % NWORK));
     }
 }
-
-// The join may be launched while the kernel that writes the parts still runs: it looks up its
-// work first and waits for the parts then.
-__device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 constexpr int kJoinThreads = 128;
 
@@ -445,39 +472,58 @@ __device__ __forceinline__ void write_row(uint16_t *o, const float (&a)[D / 32],
     for (int c = 0; c < D / 64; ++c) dst[c] = pack16<F16>(a[2 * c] * inv, a[2 * c + 1] * inv);
 }
 
-// Split items of the rows kernel, a block per row: the parts (up to a hundred and more) are
-// shared among its warps.  Grid: (items, rows of an item).
+// Items that reach beyond a block's stretch, from the records that the blocks left.  Grid:
+// (blocks of the kernel that wrote the parts, rows of an item / rows_per_block).  slot_tokens 0:
+// items of 16 (token, head) rows; else two slots of 128 rows, slot_tokens tokens each.  A warp
+// joins a row; where a row has many parts (up to one per block), the block's warps share it.
+// (A kernel that found the cut items by itself, as the blocks do, took 82 us for 147 of them
+// with a block per 4 rows, where reading and writing them takes 6.)
 template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) gqa_rows_join_kernel(const GqaParams p) {
-    constexpr int ROWS = RowsCfg<D>::ROWS, WARPS = kJoinThreads / 32, CPT = D / 32;
-    __shared__ ScanScratch scan;
+__global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams p, int slot_tokens, int rows_per_block) {
+    constexpr int WARPS = kJoinThreads / 32, CPT = D / 32;
     __shared__ float s_a[WARPS][32][CPT + 1];
-    WorkItem w;
-    if (!find_work<kJoinThreads, false>(p.b, blockIdx.x, scan, w) || w.segs <= 1) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y, G = p.b.G;
-    const int64_t r = static_cast<int64_t>(w.i) * ROWS + row, all = static_cast<int64_t>(w.s.n) * G;
-    if (r >= all) return;
-    const int t = static_cast<int>(r / G), g = static_cast<int>(r % G);
-    const int64_t last = min(static_cast<int64_t>(w.i + 1) * ROWS, all) - 1;
-    const int t_end = (visible_keys(p.b, w.s, static_cast<int>(last / G)) + p.b.tile - 1) / p.b.tile;
-    const int64_t first = static_cast<int64_t>(w.slot) * ROWS + row;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.b.G;
     wait_for_parts();
-    float a[CPT], sum;
-    join_share<D>(p, t_end > 0 ? (t_end + w.L - 1) / w.L : 0,   // the segments that were written
-                  [&](int s) { return first + static_cast<int64_t>(s) * ROWS; }, warp, WARPS, a, sum);
+    const JoinItem it = p.joins[blockIdx.x];
+    if (it.parts == 0) return;
+    const int rows = slot_tokens ? 256 : RowsCfg<D>::ROWS;
+    const bool shared = it.parts >= 2 * WARPS;
+    const SeqInfo seq{it.q0, it.n, it.m, 0};
+    for (int k = shared ? 0 : warp; k < rows_per_block; k += shared ? 1 : WARPS) {
+        const int row = blockIdx.y * rows_per_block + k;
+        int64_t t;
+        int g;
+        if (slot_tokens) {
+            const int tl = (row & 127) / G;
+            if (tl >= slot_tokens) continue;
+            g = (row & 127) % G;
+            t = static_cast<int64_t>(it.i) * 2 * slot_tokens + (row >> 7) * slot_tokens + tl;
+        } else {
+            const int64_t flat = static_cast<int64_t>(it.i) * rows + row;
+            t = flat / G, g = static_cast<int>(flat % G);
+        }
+        if (t >= it.n) continue;
+        float a[CPT], sum;
+        // the first part may sit in its block's second slot, the others in the first one of the blocks behind
+        join_share<D>(p, it.parts, [&](int x) { return static_cast<int64_t>(x == 0 ? it.slot0 : (it.slot0 & ~1) + 2 * x) * rows + row; },
+                      shared ? warp : 0, shared ? WARPS : 1, a, sum);
+        if (shared) {
+            __syncthreads();
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) s_a[warp][lane][c] = a[c];
-    s_a[warp][lane][CPT] = sum;
-    __syncthreads();
-    if (warp > 0) return;
+            for (int c = 0; c < CPT; ++c) s_a[warp][lane][c] = a[c];
+            s_a[warp][lane][CPT] = sum;
+            __syncthreads();
+            if (warp > 0) continue;
 #pragma unroll
-    for (int k = 1; k < WARPS; ++k) {
+            for (int j = 1; j < WARPS; ++j) {
 #pragma unroll
-        for (int c = 0; c < CPT; ++c) a[c] += s_a[k][lane][c];
-        sum += s_a[k][lane][CPT];
+                for (int c = 0; c < CPT; ++c) a[c] += s_a[j][lane][c];
+                sum += s_a[j][lane][CPT];
+            }
+        }
+        write_row<D, F16>(p.o + (static_cast<int64_t>(it.q0) + t) * p.o_st + (static_cast<int64_t>(it.h) * G + g) * p.o_sh, a, sum,
+                          visible_keys(p.b, seq, static_cast<int>(t)) == 0);
     }
-    write_row<D, F16>(p.o + (static_cast<int64_t>(w.s.q0) + t) * p.o_st + (static_cast<int64_t>(w.h) * G + g) * p.o_sh, a, sum,
-                      visible_keys(p.b, w.s, t) == 0);
 }
 
 }  // namespace lite

@@ -36,17 +36,8 @@
 
 namespace lite {
 
-// What a block leaves for the join about the item that reaches beyond its stretch.
-struct JoinItem {
-    int parts, slot0;      // parts 0: there is none
-    int row0, tokens;      // rows of q and o of its first token; its tokens
-    int h, vis0;           // keys that the first token sees
-    int pad[2];
-};
-
 struct TileParams {
     GqaParams a;
-    JoinItem *joins;                    // workspace: [blocks]
     const uint16_t *v;                  // values in global memory (rows of values that are not finite)
     int64_t v_page, v_token, v_head;    // strides, elements (packed: v_token, v_head)
     int slot_tokens;                    // tokens of a slot: 128 / G
@@ -236,61 +227,15 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         ptx::regs_dec<C::REG_CTRL>();
         if (warp == 3) {
             // -------------------------------------------------------- work items
-            WorkCursor cur;
-            const bool line = stretch > 0;
-            if (p.joins && lane == 0) p.joins[blockIdx.x] = JoinItem{};
-            cur.start(pb, line, lane);
-            int64_t x = line ? blockIdx.x * stretch : 0;   // the next place on the line, or round of whole items
-            const int64_t x_end = x + stretch;
+            BlockWalk walk;
+            walk.start(pb, stretch, p.a.joins, lane);
             int published = 0;
             bool more = true, ok = true;
             auto publish = [&]() {     // the block's next item (or the end of them)
-                LineItem it;
-                int t0 = 0, t1 = 0, us0 = 0, us1 = 0, v0 = 0, v1 = 0, slot = 0;
-                bool whole = true;
-                while (true) {
-                    SeqInfo s;
-                    int b;
-                    int64_t first;
-                    if (line) {
-                        more = x < x_end && cur.find(pb, true, lane, x, b, s, first);
-                        if (!more) break;
-                        line_item(pb, b, s, first, x, it);
-                        const bool mine = line_tiles(pb, it, stretch, blockIdx.x, t0, t1, whole);
-                        slot = line_slot(it, stretch, blockIdx.x);
-                        x = it.to;
-                        if (it.from >= blockIdx.x * stretch && it.to > x_end) {   // begins here, reaches beyond
-                            int parts = 0, slot0 = 0;
-                            bool all = false;
-                            // the stretches with tiles of the item are consecutive
-                            for (int64_t y = blockIdx.x; y * stretch < it.to && !all; ++y) {
-                                int c0, c1;
-                                if (!line_tiles(pb, it, stretch, y, c0, c1, all)) continue;
-                                if (parts++ == 0) slot0 = line_slot(it, stretch, y);
-                            }
-                            if (!all && lane == 0) {           // else one block writes it
-                                JoinItem *join = p.joins + blockIdx.x;
-                                join->parts = parts, join->slot0 = slot0;
-                                join->row0 = it.s.q0 + it.i * pb.unit_tokens;
-                                join->tokens = min(pb.unit_tokens, it.s.n - it.i * pb.unit_tokens);
-                                join->h = it.h;
-                                join->vis0 = pb.causal ? it.s.m - it.s.n + it.i * pb.unit_tokens + 1 : it.s.m;
-                            }
-                        }
-                        if (mine) break;
-                    } else {
-                        const int grid = static_cast<int>(gridDim.x), blk = static_cast<int>(blockIdx.x);
-                        const int64_t item = x * grid + ((x & 1) ? grid - 1 - blk : blk);
-                        ++x;
-                        more = cur.find(pb, false, lane, item, b, s, first);
-                        if (!more) break;
-                        const int y = static_cast<int>(item - first);
-                        it.s = s, it.b = b, it.h = y % pb.Hk, it.i = seq_blocks(pb, s.n) - 1 - y / pb.Hk;
-                        it.keys = block_keys(pb, s, it.i);
-                        t1 = (it.keys + BN - 1) / BN;
-                        break;
-                    }
-                }
+                more = walk.next(pb, p.a.joins, lane);
+                const LineItem &it = walk.it;
+                const int t0 = walk.t0, t1 = walk.t1;
+                int us0 = 0, us1 = 0, v0 = 0, v1 = 0;
                 const int tok0 = more ? it.i * 2 * p.slot_tokens : 0;
                 int lim_lo = 0;
                 if (more) {
@@ -312,7 +257,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     tw.valid = more ? 1 : 0;
                     if (more) {
                         tw.k0 = it.s.k0, tw.q0 = it.s.q0, tw.n = it.s.n, tw.m = it.s.m, tw.b = it.b, tw.h = it.h;
-                        tw.tok0 = tok0, tw.whole = whole ? 1 : 0, tw.slot = slot, tw.t_lo = t0;
+                        tw.tok0 = tok0, tw.whole = walk.whole ? 1 : 0, tw.slot = walk.slot, tw.t_lo = t0;
                         tw.us0 = us0, tw.us1 = us1, tw.n_u = max(us0, us1);
                         tw.lim_lo = lim_lo, tw.lim_hi = max(v0, v1);
                         tw.mask_tile = lim_lo / BN, tw.e_mask = max(0, lim_lo / BN - t0);
@@ -399,11 +344,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (!tw.valid) break;
                 const int n_e = (tw.n_u + 1) / 2, us0 = tw.us0, us1 = tw.us1, t_lo = tw.t_lo, e_mask = tw.e_mask, h = tw.h;
                 const int row0 = tw.q0 + tw.tok0;
-                WorkItem w;
-                w.b = tw.b;
-                w.h = h;
-                w.s.k0 = tw.k0;
-                KvTiles<BN, DCH> tiles(pb, w, tw.lim_hi);
+                KvTiles<BN, DCH> tiles(pb, tw.k0, tw.b, h, tw.lim_hi);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(w_empty(at));
                 int pg = n_e > 0 ? tiles.page_of(t_lo, lane) : -1;
@@ -796,30 +737,6 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 2) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
-}
-
-// Items that lie across the end of a block's stretch, from what the blocks left about them.
-// Grid: (blocks of the tile kernel, 256 / kTileJoinRows), a warp per row at a time.  (Finding the
-// items again here took longer than joining them: 82 us for 147 of them, a block per 4 rows.)
-constexpr int kTileJoinRows = 16;
-
-template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) gqa_tile_join_kernel(const TileParams p) {
-    wait_for_parts();
-    const JoinItem it = p.joins[blockIdx.x];
-    if (it.parts == 0) return;
-    const int G = p.a.b.G;
-    for (int k = threadIdx.x >> 5; k < kTileJoinRows; k += kJoinThreads / 32) {
-        const int row = blockIdx.y * kTileJoinRows + k;
-        const int tl = (row & 127) / G, g = (row & 127) % G;
-        const int t = (row >> 7) * p.slot_tokens + tl;
-        if (tl >= p.slot_tokens || t >= it.tokens) continue;
-        float a[D / 32], sum;
-        // the first part may sit in its block's second slot, the others in the first one of the blocks behind
-        join_share<D>(p.a, it.parts, [&](int x) { return static_cast<int64_t>(x == 0 ? it.slot0 : (it.slot0 & ~1) + 2 * x) * 256 + row; }, 0, 1, a, sum);
-        write_row<D, F16>(p.a.o + (static_cast<int64_t>(it.row0) + t) * p.a.o_st + (static_cast<int64_t>(it.h) * G + g) * p.a.o_sh, a, sum,
-                          (p.a.b.causal ? it.vis0 + t : it.vis0) <= 0);
-    }
 }
 
 }  // namespace lite

@@ -144,10 +144,14 @@ struct Division {
     bool tile;            // the 256-row tcgen05 kernel, or the 16-row kernel
     int rows;             // query rows of an item
     int64_t items;        // most work items there can be
-    int target;           // split target, 0: no splitting
+    int blocks;           // persistent blocks
+    bool split;           // items may be cut
     size_t workspace;
 };
-constexpr int kRowsMinTiles = 4;      // shortest segment, tiles of 64 keys
+// In keys, measured: the turn from one item to the next, and what partial outputs and their join cost.
+constexpr int kTileItemCost = 256, kTileJoinCost = 1280, kTileMinStretch = 512;
+constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 256;
+constexpr int kManyItems = 8;   // items per block from which whole items come out even
 
 Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_new, int64_t max_keys) {
     const int64_t G = pl->Hq / pl->Hk;
@@ -155,31 +159,35 @@ Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_
     Division dv;
     dv.tile = max_new * G > RowsCfg<128>::ROWS;
     int64_t least;        // items of a batch without padding
+    int most;             // blocks that run at the same time
     if (dv.tile) {
         const int64_t per = 2 * (128 / G);
         dv.rows = 256;
         dv.items = pl->Hk * std::min((tokens + B * (per - 1)) / per, tokens);
         least = pl->Hk * ((tokens + per - 1) / per);
-        dv.target = pl->sms;          // one block per SM
-        if (least >= 8 * pl->sms || max_keys <= kJoinCost) dv.target = 0;   // whole items come out even, or splitting cannot pay
+        most = pl->sms;
     } else {
         const int64_t rows = RowsCfg<128>::ROWS;
         dv.rows = RowsCfg<128>::ROWS;
         dv.items = pl->Hk * std::min((tokens * G + B * (rows - 1)) / rows, tokens * G);
         least = pl->Hk * ((tokens * G + rows - 1) / rows);
-        dv.target = 2 * pl->sms;      // two blocks per SM
-        if (least >= 2 * dv.target || max_keys <= kRowsMinTiles * RowsCfg<128>::BN) dv.target = 0;
+        most = 2 * pl->sms;
     }
-    dv.workspace = static_cast<size_t>(2 * dv.target) * dv.rows * (pl->d + 2) * 4u + static_cast<size_t>(dv.target) * sizeof(JoinItem);
+    dv.split = least < kManyItems * most && max_keys > (dv.tile ? kTileJoinCost : kRowsJoinCost);
+    // no more blocks than there can be items, unless items may be cut
+    dv.blocks = dv.split ? most : static_cast<int>(std::min<int64_t>(dv.items, most));
+    dv.workspace = dv.split ? static_cast<size_t>(dv.blocks) * (2 * static_cast<size_t>(dv.rows) * (pl->d + 2) * 4u + sizeof(JoinItem)) : 0;
     return dv;
 }
 
 // The kernel that joins split items, launched so that it may begin before the one in front of
 // it has ended (it waits for that one's results itself).
-template <typename K, typename P>
-int launch_join(K kernel, dim3 grid, const P &p, cudaStream_t s) {
+template <int D, bool F16>
+int launch_join(const GqaParams &p, const Division &dv, int slot_tokens, cudaStream_t s) {
+    if (!dv.split) return LITE_OK;
+    const int rows_per_block = dv.tile ? 16 : 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(dv.blocks, dv.rows / rows_per_block);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
@@ -187,7 +195,7 @@ int launch_join(K kernel, dim3 grid, const P &p, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const int rc = cuda_err(cudaLaunchKernelEx(&cfg, kernel, p));
+    const int rc = cuda_err(cudaLaunchKernelEx(&cfg, gqa_join_kernel<D, F16>, p, slot_tokens, rows_per_block));
     if (rc != LITE_OK) cudaGetLastError();
     else g_launches.fetch_add(1);
     return rc;
@@ -200,10 +208,10 @@ int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMa
     static std::atomic<bool> done[kMaxDevices];
     int rc = allow_smem(gqa_rows_kernel<D, F16>, done, pl->device, C::SMEM_BYTES);
     if (rc != LITE_OK) return rc;
-    gqa_rows_kernel<D, F16><<<static_cast<unsigned>(dv.items + dv.target), C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
+    gqa_rows_kernel<D, F16><<<dv.blocks, C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
     g_launches.fetch_add(1);
-    if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target) return rc;
-    return launch_join(gqa_rows_join_kernel<D, F16>, dim3(static_cast<unsigned>(dv.items), C::ROWS), p, s);
+    rc = cuda_err(cudaGetLastError());
+    return rc == LITE_OK ? launch_join<D, F16>(p, dv, 0, s) : rc;
 }
 
 template <int D, bool F16>
@@ -222,12 +230,10 @@ int launch_tile(const lite_attn_gqa *pl, const CUtensorMap &tq, const CUtensorMa
     }
     int rc = allow_smem(gqa_tile_kernel<D, F16>, done, pl->device, C::SMEM_BYTES);
     if (rc != LITE_OK) return rc;
-    // persistent blocks, one per SM; no more than there can be items, unless items may be cut
-    const unsigned grid = static_cast<unsigned>(dv.target ? pl->sms : std::min<int64_t>(dv.items, pl->sms));
-    gqa_tile_kernel<D, F16><<<grid, C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
+    gqa_tile_kernel<D, F16><<<dv.blocks, C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
     g_launches.fetch_add(1);
-    if ((rc = cuda_err(cudaGetLastError())) != LITE_OK || !dv.target || grid < 2) return rc;
-    return launch_join(gqa_tile_join_kernel<D, F16>, dim3(grid, 256 / kTileJoinRows), p, s);
+    rc = cuda_err(cudaGetLastError());
+    return rc == LITE_OK ? launch_join<D, F16>(p.a, dv, p.slot_tokens, s) : rc;
 }
 
 // Attention of q over the cache (c) or packed rows (k, v).
@@ -236,7 +242,7 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
               void *workspace, size_t workspace_bytes, cudaStream_t s) {
     const int G = pl->Hq / pl->Hk;
     const Division dv = divide(pl, b.B, q.tokens, max_new, c ? b.max_keys : b.Tk);
-    if (dv.items + dv.target >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
+    if (dv.items >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
     if (workspace_bytes < dv.workspace) return LITE_ERR_INVALID_ARG;
     if (dv.workspace && !device_range_ok(workspace, dv.workspace, pl->device)) return LITE_ERR_INVALID_ARG;
     if (dv.workspace && !apart(workspace, dv.workspace, o.ptr, rows_bytes(o, pl->Hq, pl->d))) return LITE_ERR_INVALID_ARG;
@@ -246,9 +252,12 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     b.status = pl->status;
     b.unit_rows = dv.tile ? 0 : dv.rows;
     b.unit_tokens = dv.tile ? 2 * (128 / G) : 0;
-    b.tile = dv.tile ? 128 : RowsCfg<128>::BN;
-    b.split_target = dv.target;
-    b.min_tiles = kRowsMinTiles;
+    const int tile = dv.tile ? 128 : RowsCfg<128>::BN;
+    b.tile_shift = dv.tile ? 7 : 6;
+    b.may_split = dv.split ? 1 : 0;
+    b.item_cost = dv.tile ? kTileItemCost : kRowsItemCost;
+    b.join_cost = dv.tile ? kTileJoinCost : kRowsJoinCost;
+    b.min_stretch = dv.tile ? kTileMinStretch : kRowsMinStretch;
     TileParams t;
     std::memset(&t, 0, sizeof t);
     GqaParams &p = t.a;
@@ -257,10 +266,13 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     p.o = static_cast<uint16_t *>(o.ptr);
     p.q_st = q.stride_token, p.q_sh = q.stride_head, p.o_st = o.stride_token, p.o_sh = o.stride_head;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    p.ws_ml = static_cast<float *>(workspace);
-    p.ws_o = p.ws_ml + static_cast<size_t>(2 * dv.target) * dv.rows * 2;
-    t.joins = dv.target ? reinterpret_cast<JoinItem *>(p.ws_o + static_cast<size_t>(2 * dv.target) * dv.rows * pl->d) : nullptr;
-    const int box = c ? std::min(c->page, b.tile) : b.tile;
+    if (dv.split) {
+        const size_t rows = 2 * static_cast<size_t>(dv.blocks) * dv.rows;
+        p.ws_o = static_cast<float *>(workspace);
+        p.ws_ml = p.ws_o + rows * pl->d;
+        p.joins = reinterpret_cast<JoinItem *>(p.ws_ml + rows * 2);
+    }
+    const int box = c ? std::min(c->page, tile) : tile;
     CUtensorMap tq, tk, tv;
     std::memset(&tq, 0, sizeof tq);
     std::memset(&tk, 0, sizeof tk);

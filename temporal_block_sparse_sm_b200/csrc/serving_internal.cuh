@@ -6,18 +6,19 @@
 // queries are the last n of the sequence's positions: query token t sees keys
 // [0, m - n + t] (causal) or all m.
 //
-// Lengths live on the device, so that a captured graph can be replayed on other lengths;
-// the host knows only upper bounds.  Every block finds its own work item by a scan over
-// the sequences (a few loads per thread), and blocks behind the last item return at once.
+// Lengths live on the device, so that a captured graph can be replayed on other lengths; the
+// host knows only upper bounds.  The kernels' blocks are persistent, and one warp of each walks
+// the batch for the block's items (BlockWalk).
 //
-// Splitting along the keys.  With few rows and long caches there are fewer (sequence, key
-// head, row block) items than SMs.  Each item is then cut into segments of L key tiles,
-// L = max(min_tiles, ceil(W / target)), W = all tiles of all items; the number of segments
-// is at most target + items however ragged the lengths are.  A segment leaves its
-// unnormalised output, running maximum and sum in the workspace, and a second kernel joins
-// them.  Items of one segment write their output themselves and use no workspace; split
-// items have more than L tiles, so there are at most 2 * target segments of them, which
-// bounds the workspace whatever the batch.
+// Division among the blocks.  A batch of many items (block of query rows, key head) is dealt
+// out whole, in order of length within a sequence, back and forth over the blocks.  With few
+// items the batch is laid out on a line instead, an item taking as many units as its last row
+// sees keys, and item_cost for its start and end; each block takes an equal stretch of the line,
+// cut at the nearest tile.  A block then has at most two partial items, at the ends of its
+// stretch: a partial item's unnormalised output, running maximum and sum go to one of the block's
+// two workspace slots, which bounds the workspace whatever the batch, and a second kernel joins
+// the at most one item per block that reaches beyond its stretch, from a record that the block
+// leaves about it.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,9 +44,11 @@ struct GqaBatch {
     int table_w, page_shift;
     int unit_rows;         // query rows (token, head of the group) of a work item, or 0: unit_tokens tokens
     int unit_tokens;
-    int tile;              // keys of a tile
-    int split_target;      // 0: no splitting
-    int min_tiles;
+    int tile_shift;        // log2 of the keys of a tile
+    int may_split;         // items may be cut
+    // in keys: what an item costs beside its keys, what partial outputs and their join cost, and
+    // the shortest stretch (more than a tile, so that no stretch inside an item is without one)
+    int item_cost, join_cost, min_stretch;
 };
 
 struct SeqInfo {
@@ -84,122 +87,6 @@ __device__ __forceinline__ int seq_blocks(const GqaBatch &p, int n) {
     return (n + p.unit_tokens - 1) / p.unit_tokens;
 }
 
-// One block's work: row block i of key head h of sequence b, key tiles [seg * L, (seg + 1) * L).
-struct WorkItem {
-    SeqInfo s;
-    int b, h, i;
-    int seg, segs, L;      // segs > 1: a split item
-    int slot;              // its workspace slot (split items), or the slot of its first segment
-    int found;
-};
-
-struct ScanScratch {
-    int64_t sum[32];
-    int cnt[32], spl[32];
-    WorkItem w;
-};
-
-__device__ __forceinline__ int seq_tiles(const GqaBatch &p, int m) {   // a sequence without keys counts as one
-    return m > 0 ? static_cast<int>((static_cast<int64_t>(m) + p.tile - 1) / p.tile) : 1;
-}
-
-// Key tiles of a segment (the whole block of NT threads; the same in every block).
-template <int NT>
-__device__ __forceinline__ int segment_tiles(const GqaBatch &p, ScanScratch &sc) {
-    if (p.split_target <= 0) return 1 << 30;   // no item has that many tiles: one segment each
-    constexpr int NW = NT / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    for (int b = p.B == 1 ? 0 : threadIdx.x; b < p.B; b += NT) {
-        const SeqInfo s = seq_info(p, b);
-        sum += static_cast<int64_t>(p.Hk) * seq_blocks(p, s.n) * seq_tiles(p, s.m);
-    }
-    if (p.B > 1) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (lane == 0) sc.sum[warp] = sum;
-        __syncthreads();
-        sum = 0;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) sum += sc.sum[k];
-    }
-    const int64_t l = (sum + p.split_target - 1) / p.split_target;
-    return static_cast<int>(l < p.min_tiles ? p.min_tiles : l > (1 << 30) ? (1 << 30) : l);
-}
-
-// Work item y of sequence b, whose first segment has workspace slot `slot0`.  The order is
-// by row block, those with most keys first, then by key head: blocks that run at the same
-// time have about the same work, and the last ones are short.
-template <bool SEGMENTS>
-__device__ __forceinline__ void decode_item(const GqaBatch &p, int b, const SeqInfo &s, int L, int y, int slot0, WorkItem &w) {
-    const int nb = seq_blocks(p, s.n);
-    w.segs = (seq_tiles(p, s.m) + L - 1) / L;
-    const int per = SEGMENTS ? w.segs : 1;
-    w.s = s;
-    w.b = b;
-    w.seg = y % per;
-    const int item = y / per;
-    w.h = item % p.Hk;
-    w.i = nb - 1 - item / p.Hk;
-    w.L = L;
-    w.slot = slot0 + item * w.segs + w.seg;
-}
-
-// The x-th work item of the batch (SEGMENTS: the x-th segment), found by the whole block of
-// NT threads; false when there are fewer.
-template <int NT, bool SEGMENTS>
-__device__ __forceinline__ bool find_work(const GqaBatch &p, int x, ScanScratch &sc, WorkItem &w) {
-    constexpr int NW = NT / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int L = segment_tiles<NT>(p, sc);
-    if (p.B == 1) {
-        const SeqInfo s = seq_info(p, 0);
-        const int items = p.Hk * seq_blocks(p, s.n);
-        if (x >= items * (SEGMENTS ? (seq_tiles(p, s.m) + L - 1) / L : 1)) return false;
-        decode_item<SEGMENTS>(p, 0, s, L, x, 0, w);
-        return true;
-    }
-    if (threadIdx.x == 0) sc.w.found = 0;
-    int base = 0, slot_base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += NT) {
-        const int b = b0 + threadIdx.x;
-        SeqInfo s = {0, 0, 0, 0};
-        int cnt = 0, spl = 0;
-        if (b < p.B) {
-            s = seq_info(p, b);
-            const int items = p.Hk * seq_blocks(p, s.n), segs = (seq_tiles(p, s.m) + L - 1) / L;
-            cnt = SEGMENTS ? items * segs : items;
-            spl = segs > 1 ? items * segs : 0;
-        }
-        int ci = cnt, si = spl;   // inclusive scans over the warp
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(0xFFFFFFFFu, ci, o), c = __shfl_up_sync(0xFFFFFFFFu, si, o);
-            if (lane >= o) ci += a, si += c;
-        }
-        if (lane == 31) sc.cnt[warp] = ci, sc.spl[warp] = si;
-        __syncthreads();
-        int before = base, sbefore = slot_base, total = 0, stotal = 0;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            if (k < warp) before += sc.cnt[k], sbefore += sc.spl[k];
-            total += sc.cnt[k], stotal += sc.spl[k];
-        }
-        const int lo = before + ci - cnt;
-        if (cnt > 0 && x >= lo && x < lo + cnt) {
-            decode_item<SEGMENTS>(p, b, s, L, x - lo, sbefore + si - spl, w);
-            sc.w = w;
-            sc.w.found = 1;
-        }
-        __syncthreads();
-        if (x < base + total) break;
-        base += total;
-        slot_base += stotal;
-    }
-    w = sc.w;
-    return w.found != 0;
-}
-
 // Keys that query token t of a sequence sees (0: none).
 __device__ __forceinline__ int visible_keys(const GqaBatch &p, const SeqInfo &s, int t) {
     if (!p.causal) return s.m;
@@ -207,42 +94,46 @@ __device__ __forceinline__ int visible_keys(const GqaBatch &p, const SeqInfo &s,
     return v < 0 ? 0 : v;
 }
 
-// ---------------------------------------------------------------- division among persistent blocks
-// Items of the tile kernel have very different lengths.  A batch of many items is dealt out
-// whole, in order of length, back and forth over the blocks.  With few items the batch is
-// laid out on a line instead, an item taking as many units as its last row sees keys, and
-// kItemCost for its start and end; each block takes an equal stretch of the line, cut at the
-// next tile boundary.  A block then has at most two partial items, at the ends of its stretch,
-// so the workspace holds two slots per block, and at most one item per block boundary is
-// joined afterwards.
-constexpr int kItemCost = 256;      // measured: the turn from one item to the next costs about two tiles
-constexpr int kMinStretch = 512;    // more than a tile, so that no stretch inside an item is without one
-constexpr int kJoinCost = 1280;     // keys whose time partial outputs and their join cost
+// a / b for a, b >= 0; in 32 bits where they fit (a 64-bit division takes about 100 instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
 // Keys that the last row of block i sees.
 __device__ __forceinline__ int block_keys(const GqaBatch &p, const SeqInfo &s, int i) {
-    const int last = min((i + 1) * p.unit_tokens, s.n) - 1;
+    const int last = p.unit_rows ? static_cast<int>((min(static_cast<int64_t>(i + 1) * p.unit_rows, static_cast<int64_t>(s.n) * p.G) - 1) / p.G)
+                                 : min((i + 1) * p.unit_tokens, s.n) - 1;
     return visible_keys(p, s, last);
 }
-
-// Units of the first k block groups (last rows first) of one head of a sequence.
+// Units of block i, and of the first k blocks (last rows first) of one head of a sequence.  Blocks
+// of a few rows count all m keys.
+__device__ __forceinline__ int64_t block_units(const GqaBatch &p, const SeqInfo &s, int i) {
+    return static_cast<int64_t>(p.item_cost) + (p.unit_rows ? s.m : block_keys(p, s, i));
+}
 __device__ __forceinline__ int64_t group_units(const GqaBatch &p, const SeqInfo &s, int nb, int k) {
     if (k <= 0) return 0;
-    if (!p.causal) return static_cast<int64_t>(k) * (static_cast<int64_t>(s.m) + kItemCost);
+    if (!p.causal || p.unit_rows) return static_cast<int64_t>(k) * (static_cast<int64_t>(s.m) + p.item_cost);
     // block nb - 1 sees m keys; block x - 1 < nb - 1 sees m - n + x * unit_tokens, 0 at least
     const int64_t a = static_cast<int64_t>(s.m) - s.n, tb = p.unit_tokens;
     int64_t lo = nb - k + 1;
-    const int64_t first = a > 0 ? 1 : (-a) / tb + 1;
+    const int64_t first = a > 0 ? 1 : quotient(-a, tb) + 1;
     lo = lo < first ? first : lo;
     const int64_t hi = nb - 1;
-    int64_t sum = static_cast<int64_t>(k) * kItemCost + s.m;
+    int64_t sum = static_cast<int64_t>(k) * p.item_cost + s.m;
     if (lo <= hi) sum += (hi - lo + 1) * a + tb * ((lo + hi) * (hi - lo + 1) / 2);
     return sum;
 }
+
+struct ScanScratch {
+    int64_t sum[32];
+    int items[32], longest[32];
+};
+
 // Units of a block's stretch, 0: items are dealt out whole.  The same in every block (of NT threads).
 template <int NT>
 __device__ __forceinline__ int64_t stretch_units(const GqaBatch &p, int blocks, ScanScratch &sc) {
-    if (p.split_target <= 0) return 0;
+    if (!p.may_split) return 0;
     constexpr int NW = NT / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t units = 0;
@@ -261,25 +152,25 @@ __device__ __forceinline__ int64_t stretch_units(const GqaBatch &p, int blocks, 
             items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
             longest = max(longest, __shfl_xor_sync(0xFFFFFFFFu, longest, o));
         }
-        if (lane == 0) sc.sum[warp] = units, sc.cnt[warp] = items, sc.spl[warp] = longest;
+        if (lane == 0) sc.sum[warp] = units, sc.items[warp] = items, sc.longest[warp] = longest;
         __syncthreads();
         units = 0, items = 0, longest = 0;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) units += sc.sum[k], items += sc.cnt[k], longest = max(longest, sc.spl[k]);
-        __syncthreads();
+        for (int k = 0; k < NW; ++k) units += sc.sum[k], items += sc.items[k], longest = max(longest, sc.longest[k]);
     }
-    const int64_t even = max((units + blocks - 1) / blocks, static_cast<int64_t>(kMinStretch));
+    const int64_t even = max(quotient(units + blocks - 1, blocks), static_cast<int64_t>(p.min_stretch));
     // Dealt out whole, one sequence's items fall off in length to the shortest, and the blocks end
     // within one of those of each other; those of several sequences within about half the longest.
-    const int64_t rounds = (items + blocks - 1) / blocks, most = static_cast<int64_t>(longest) + kItemCost;
+    const int64_t rounds = (items + blocks - 1) / blocks, most = static_cast<int64_t>(longest) + p.item_cost;
     const int64_t whole = max(most, min(rounds * most, even + (p.B == 1 ? static_cast<int64_t>(shortest) : most / 2)));
-    return even + kJoinCost < whole ? even : 0;
+    return even + p.join_cost < whole ? even : 0;
 }
 
-// An item's place: its sequence, block, head, and stretch [from, to) of the line.
+// An item: its sequence, block of rows and head, the keys that its last row sees, and its stretch
+// [from, to) of the line.
 struct LineItem {
     SeqInfo s;
-    int b, i, h, keys;     // keys that its last row sees
+    int b, i, h, keys;
     int64_t from, to;
 };
 __device__ __forceinline__ void line_item(const GqaBatch &p, int b, const SeqInfo &s, int64_t base, int64_t x, LineItem &it) {
@@ -295,26 +186,37 @@ __device__ __forceinline__ void line_item(const GqaBatch &p, int b, const SeqInf
     it.b = b;
     it.i = nb - 1 - lo;
     it.keys = block_keys(p, s, it.i);
-    const int64_t start = p.Hk * group_units(p, s, nb, lo), len = static_cast<int64_t>(it.keys) + kItemCost;
-    it.h = static_cast<int>((at - start) / len);
+    const int64_t start = p.Hk * group_units(p, s, nb, lo), len = block_units(p, s, it.i);
+    it.h = static_cast<int>(quotient(at - start, len));
     it.from = base + start + it.h * len;
     it.to = it.from + len;
 }
+__device__ __forceinline__ int tiles_of(const GqaBatch &p, int keys) {
+    return static_cast<int>((static_cast<int64_t>(keys) + (1 << p.tile_shift) - 1) >> p.tile_shift);
+}
 // The tiles [t0, t1) of an item that fall to stretch q; false when there are none.  `whole`: all of them do.
 __device__ __forceinline__ bool line_tiles(const GqaBatch &p, const LineItem &it, int64_t stretch, int64_t q, int &t0, int &t1, bool &whole) {
-    const int nt = static_cast<int>((static_cast<int64_t>(it.keys) + p.tile - 1) / p.tile);
+    const int nt = tiles_of(p, it.keys);
     auto cut = [&](int64_t x) {          // a boundary at x: the nearest tile
-        const int64_t t = (x - it.from + p.tile / 2) / p.tile;
+        const int64_t t = (x - it.from + (1 << (p.tile_shift - 1))) >> p.tile_shift;
         return x <= it.from ? 0 : x >= it.to || t > nt ? nt : static_cast<int>(t);
     };
     t0 = cut(q * stretch);
     t1 = cut((q + 1) * stretch);
-    whole = t0 == 0 && t1 == nt && (nt > 0 || it.from / stretch == q);
+    // an item without tiles belongs to the stretch that it begins in
+    whole = t0 == 0 && t1 == nt && (nt > 0 || (it.from >= q * stretch && it.from < (q + 1) * stretch));
     return t1 > t0 || whole;
 }
 __device__ __forceinline__ int line_slot(const LineItem &it, int64_t stretch, int64_t q) {
     return static_cast<int>(2 * q) + (q * stretch > it.from ? 0 : 1);
 }
+
+// What a block leaves for the join about the item that reaches beyond its stretch.
+struct JoinItem {
+    int parts, slot0;      // parts 0: there is none
+    int q0, n, m, i, h;    // its sequence, block of rows and head
+    int pad;
+};
 
 // The batch walked by one warp, forwards: items by number, or by place on the line.  The lanes
 // hold 32 sequences at a time.
@@ -362,6 +264,62 @@ struct WorkCursor {
         first = __shfl_sync(0xFFFFFFFFu, lo, src);
         b = b0 + src;
         return true;
+    }
+};
+
+// The items of this block in order, for one converged warp.
+struct BlockWalk {
+    WorkCursor cur;
+    int64_t stretch, x, x_end;      // the next place on the line, or round of whole items
+    LineItem it;                    // the current item
+    int t0, t1, slot;               // its key tiles here; its workspace slot if they are not all
+    bool whole, any;
+    __device__ __forceinline__ void start(const GqaBatch &p, int64_t stretch_, JoinItem *joins, int lane) {
+        stretch = stretch_;
+        if (joins && lane == 0) joins[blockIdx.x] = JoinItem{};
+        cur.start(p, stretch > 0, lane);
+        x = blockIdx.x * stretch;
+        x_end = x + stretch;
+        any = false;
+    }
+    // Leaves the record about the stretch's last item, if it begins here and reaches beyond.  The
+    // stretches with tiles of an item are consecutive: the first is this one, or the next if the
+    // nearest tile boundary is the item's start, and the last is the one that holds the middle of
+    // its last tile.
+    __device__ __forceinline__ void record(const GqaBatch &p, JoinItem *joins, int lane) {
+        const int nt = any ? tiles_of(p, it.keys) : 0;
+        if (nt == 0 || it.to <= x_end || it.from < x_end - stretch) return;
+        const int64_t half = 1 << (p.tile_shift - 1);
+        const int64_t q0 = blockIdx.x + (x_end < it.from + half ? 1 : 0);
+        const int64_t q1 = quotient(it.from + (static_cast<int64_t>(nt) << p.tile_shift) - half - 1, stretch);
+        if (q0 < q1 && lane == 0)                // else one block writes it
+            joins[blockIdx.x] = JoinItem{static_cast<int>(q1 - q0) + 1, line_slot(it, stretch, q0), it.s.q0, it.s.n, it.s.m, it.i, it.h, 0};
+    }
+    __device__ __forceinline__ bool next(const GqaBatch &p, JoinItem *joins, int lane) {
+        SeqInfo s;
+        int b;
+        int64_t first;
+        if (stretch == 0) {         // whole items, back and forth over the blocks
+            const int grid = static_cast<int>(gridDim.x), blk = static_cast<int>(blockIdx.x);
+            const int64_t item = x * grid + ((x & 1) ? grid - 1 - blk : blk);
+            ++x;
+            if (!cur.find(p, false, lane, item, b, s, first)) return false;
+            const int y = static_cast<int>(item - first);
+            it.s = s, it.b = b, it.h = y % p.Hk, it.i = seq_blocks(p, s.n) - 1 - y / p.Hk;
+            it.keys = block_keys(p, s, it.i);
+            t0 = 0, t1 = tiles_of(p, it.keys), slot = 0, whole = true;
+            return true;
+        }
+        while (x < x_end && cur.find(p, true, lane, x, b, s, first)) {
+            line_item(p, b, s, first, x, it);
+            const bool mine = line_tiles(p, it, stretch, blockIdx.x, t0, t1, whole);
+            slot = line_slot(it, stretch, blockIdx.x);
+            x = it.to;
+            any = true;
+            if (mine) return true;
+        }
+        record(p, joins, lane);
+        return false;
     }
 };
 
