@@ -436,93 +436,130 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
 }
 
-constexpr int kJoinThreads = 128;
+// Joins the items that reach beyond a block's stretch, from the records that the blocks left:
+//   o = sum_s 2^(c (m_s - m)) O_s / sum_s 2^(c (m_s - m)) l_s  over a row's parts s.
+// slot_tokens 0: items of 16 (token, head) rows; else two slots of 128 rows, slot_tokens tokens
+// each.  The rows of all the items are shared out evenly over the grid, whatever few of the
+// `blocks` records name an item: a warp takes a row, or, of items with many parts (up to one
+// per block), 4 or 16 warps do.  (Finding the cut items again, as the blocks do, took 82 us for
+// 147 of them with a block per 4 rows; reading and writing them takes 6.)
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
 
-// Joins the parts of a row:  o = sum_s 2^(c (m_s - m)) O_s / sum_s 2^(c (m_s - m)) l_s.
-// Warp `w` of `warps` takes every warps-th part; part(s) is the workspace row of part s.  Returns
-// the sums of the warp's share in the frame of the row's maximum m.
-template <int D, typename Part>
-__device__ __forceinline__ void join_share(const GqaParams &p, int parts, Part part, int w, int warps, float (&a)[D / 32], float &sum) {
-    const int lane = threadIdx.x & 31;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
-    float mx = -INFINITY;
-    for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, ml[part(s)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams p, int slot_tokens, int blocks) {
     constexpr int CPT = D / 32;
-#pragma unroll
-    for (int c = 0; c < CPT; ++c) a[c] = 0.0f;
-    sum = 0.0f;
-#pragma unroll 4
-    for (int s = w; s < parts; s += warps) {
-        const int64_t at = part(s);
-        const float2 x = ml[at];
-        const float f = x.x == -INFINITY ? 0.0f : ptx::ex2((x.x - mx) * p.scale_log2);
-        const float *src = p.ws_o + at * D + lane * CPT;
-#pragma unroll
-        for (int c = 0; c < CPT; ++c) a[c] += f * src[c];
-        sum += f * x.y;
-    }
-}
-template <int D, bool F16>
-__device__ __forceinline__ void write_row(uint16_t *o, const float (&a)[D / 32], float sum, bool empty) {
-    const float inv = empty ? 0.0f : 1.0f / sum;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(o + (threadIdx.x & 31) * (D / 32));
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) dst[c] = pack16<F16>(a[2 * c] * inv, a[2 * c + 1] * inv);
-}
-
-// Items that reach beyond a block's stretch, from the records that the blocks left.  Grid:
-// (blocks of the kernel that wrote the parts, rows of an item / rows_per_block).  slot_tokens 0:
-// items of 16 (token, head) rows; else two slots of 128 rows, slot_tokens tokens each.  A warp
-// joins a row; where a row has many parts (up to one per block), the block's warps share it.
-// (A kernel that found the cut items by itself, as the blocks do, took 82 us for 147 of them
-// with a block per 4 rows, where reading and writing them takes 6.)
-template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams p, int slot_tokens, int rows_per_block) {
-    constexpr int WARPS = kJoinThreads / 32, CPT = D / 32;
-    __shared__ float s_a[WARPS][32][CPT + 1];
+    __shared__ int s_sum[kJoinWarps], s_units[kJoinThreads];
+    __shared__ float s_a[kJoinWarps][32][CPT + 1], s_mx[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.b.G;
-    wait_for_parts();
-    const JoinItem it = p.joins[blockIdx.x];
-    if (it.parts == 0) return;
     const int rows = slot_tokens ? 256 : RowsCfg<D>::ROWS;
-    const bool shared = it.parts >= 2 * WARPS;
-    const SeqInfo seq{it.q0, it.n, it.m, 0};
-    for (int k = shared ? 0 : warp; k < rows_per_block; k += shared ? 1 : WARPS) {
-        const int row = blockIdx.y * rows_per_block + k;
+    auto rows_at_once = [](int parts) { return parts < 8 ? kJoinWarps : parts < 64 ? kJoinWarps / 4 : 1; };
+    wait_for_parts();
+    // units (rows_at_once rows of an item) up to and with each record
+    const int parts_here = threadIdx.x < blocks ? p.joins[threadIdx.x].parts : 0;
+    int units = parts_here > 0 ? rows / rows_at_once(parts_here) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xFFFFFFFFu, units, o);
+        if (lane >= o) units += a;
+    }
+    if (lane == 31) s_sum[warp] = units;
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) units += s_sum[k];
+    s_units[threadIdx.x] = units;
+    __syncthreads();
+    const int total = s_units[kJoinThreads - 1];
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        int lo = 0, hi = blocks - 1;               // the first record with more than u units
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_units[mid] > u) hi = mid;
+            else lo = mid + 1;
+        }
+        const JoinItem it = p.joins[lo];
+        const int at_once = rows_at_once(it.parts), share = kJoinWarps / at_once;
+        const int row = (u - (lo > 0 ? s_units[lo - 1] : 0)) * at_once + warp / share;
         int64_t t;
         int g;
         if (slot_tokens) {
             const int tl = (row & 127) / G;
-            if (tl >= slot_tokens) continue;
             g = (row & 127) % G;
-            t = static_cast<int64_t>(it.i) * 2 * slot_tokens + (row >> 7) * slot_tokens + tl;
+            t = tl < slot_tokens ? static_cast<int64_t>(it.i) * 2 * slot_tokens + (row >> 7) * slot_tokens + tl : it.n;
         } else {
             const int64_t flat = static_cast<int64_t>(it.i) * rows + row;
             t = flat / G, g = static_cast<int>(flat % G);
         }
-        if (t >= it.n) continue;
-        float a[CPT], sum;
-        // the first part may sit in its block's second slot, the others in the first one of the blocks behind
-        join_share<D>(p, it.parts, [&](int x) { return static_cast<int64_t>(x == 0 ? it.slot0 : (it.slot0 & ~1) + 2 * x) * rows + row; },
-                      shared ? warp : 0, shared ? WARPS : 1, a, sum);
-        if (shared) {
-            __syncthreads();
+        float a[CPT] = {}, sum = 0.0f, mx = -INFINITY;
+        if (t < it.n) {
+            // the first part may sit in its block's second slot, the others in the first one of the blocks behind
+            auto part = [&](int x) { return static_cast<int64_t>(x == 0 ? it.slot0 : (it.slot0 & ~1) + 2 * x) * rows + row; };
+            // the outputs of four parts are asked for before their weights are known
+            constexpr int AHEAD = 4;
+            for (int s0 = warp % share; s0 < it.parts; s0 += AHEAD * share) {
+                float v[AHEAD][CPT];
+                float2 x[AHEAD];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    const int s = s0 + j * share;
+                    x[j] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c) v[j][c] = 0.0f;
+                    if (s < it.parts) {
+                        const int64_t at = part(s);
+                        x[j] = ml[at];
+#pragma unroll
+                        for (int c = 0; c < CPT; ++c) v[j][c] = p.ws_o[at * D + lane * CPT + c];
+                    }
+                }
+                // this warp's sums to the frame of the largest maximum so far
+                float top = mx;
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) top = fmaxf(top, x[j].x);
+                if (top != mx) {
+                    const float f = ptx::ex2((mx - top) * p.scale_log2);
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c) a[c] *= f;
+                    sum *= f;
+                    mx = top;
+                }
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    const float f = x[j].x == -INFINITY ? 0.0f : ptx::ex2((x[j].x - mx) * p.scale_log2);
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c) a[c] += f * v[j][c];
+                    sum += f * x[j].y;
+                }
+            }
+        }
+        if (share > 1) {
 #pragma unroll
             for (int c = 0; c < CPT; ++c) s_a[warp][lane][c] = a[c];
             s_a[warp][lane][CPT] = sum;
+            if (lane == 0) s_mx[warp] = mx;
             __syncthreads();
-            if (warp > 0) continue;
+            if (warp % share == 0) {
+                float top = mx;
+                for (int j = 1; j < share; ++j) top = fmaxf(top, s_mx[warp + j]);
 #pragma unroll
-            for (int j = 1; j < WARPS; ++j) {
+                for (int c = 0; c < CPT; ++c) a[c] = 0.0f;
+                sum = 0.0f;
+                for (int j = 0; j < share; ++j) {
+                    const float f = s_mx[warp + j] == -INFINITY ? 0.0f : ptx::ex2((s_mx[warp + j] - top) * p.scale_log2);
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) a[c] += s_a[j][lane][c];
-                sum += s_a[j][lane][CPT];
+                    for (int c = 0; c < CPT; ++c) a[c] += f * s_a[warp + j][lane][c];
+                    sum += f * s_a[warp + j][lane][CPT];
+                }
             }
         }
-        write_row<D, F16>(p.o + (static_cast<int64_t>(it.q0) + t) * p.o_st + (static_cast<int64_t>(it.h) * G + g) * p.o_sh, a, sum,
-                          visible_keys(p.b, seq, static_cast<int>(t)) == 0);
+        if (t < it.n && warp % share == 0) {
+            const SeqInfo seq{it.q0, it.n, it.m, 0};
+            const float inv = visible_keys(p.b, seq, static_cast<int>(t)) == 0 ? 0.0f : 1.0f / sum;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + (static_cast<int64_t>(it.q0) + t) * p.o_st +
+                                                         (static_cast<int64_t>(it.h) * G + g) * p.o_sh + lane * CPT);
+#pragma unroll
+            for (int c = 0; c < CPT / 2; ++c) dst[c] = pack16<F16>(a[2 * c] * inv, a[2 * c + 1] * inv);
+        }
+        if (share > 1) __syncthreads();
     }
 }
 

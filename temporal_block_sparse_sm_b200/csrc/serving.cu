@@ -183,11 +183,10 @@ Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_
 // The kernel that joins split items, launched so that it may begin before the one in front of
 // it has ended (it waits for that one's results itself).
 template <int D, bool F16>
-int launch_join(const GqaParams &p, const Division &dv, int slot_tokens, cudaStream_t s) {
+int launch_join(const lite_attn_gqa *pl, const GqaParams &p, const Division &dv, int slot_tokens, cudaStream_t s) {
     if (!dv.split) return LITE_OK;
-    const int rows_per_block = dv.tile ? 16 : 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(dv.blocks, dv.rows / rows_per_block);
+    cfg.gridDim = dim3(dv.tile ? 4 * pl->sms : pl->sms);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
@@ -195,7 +194,7 @@ int launch_join(const GqaParams &p, const Division &dv, int slot_tokens, cudaStr
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const int rc = cuda_err(cudaLaunchKernelEx(&cfg, gqa_join_kernel<D, F16>, p, slot_tokens, rows_per_block));
+    const int rc = cuda_err(cudaLaunchKernelEx(&cfg, gqa_join_kernel<D, F16>, p, slot_tokens, dv.blocks));
     if (rc != LITE_OK) cudaGetLastError();
     else g_launches.fetch_add(1);
     return rc;
@@ -211,7 +210,7 @@ int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMa
     gqa_rows_kernel<D, F16><<<dv.blocks, C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
     g_launches.fetch_add(1);
     rc = cuda_err(cudaGetLastError());
-    return rc == LITE_OK ? launch_join<D, F16>(p, dv, 0, s) : rc;
+    return rc == LITE_OK ? launch_join<D, F16>(pl, p, dv, 0, s) : rc;
 }
 
 template <int D, bool F16>
@@ -233,7 +232,7 @@ int launch_tile(const lite_attn_gqa *pl, const CUtensorMap &tq, const CUtensorMa
     gqa_tile_kernel<D, F16><<<dv.blocks, C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
     g_launches.fetch_add(1);
     rc = cuda_err(cudaGetLastError());
-    return rc == LITE_OK ? launch_join<D, F16>(p.a, dv, p.slot_tokens, s) : rc;
+    return rc == LITE_OK ? launch_join<D, F16>(pl, p.a, dv, p.slot_tokens, s) : rc;
 }
 
 // Attention of q over the cache (c) or packed rows (k, v).
@@ -242,7 +241,7 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
               void *workspace, size_t workspace_bytes, cudaStream_t s) {
     const int G = pl->Hq / pl->Hk;
     const Division dv = divide(pl, b.B, q.tokens, max_new, c ? b.max_keys : b.Tk);
-    if (dv.items >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
+    if (dv.items >= (int64_t(1) << 31) || dv.blocks > kJoinThreads) return LITE_ERR_UNSUPPORTED;
     if (workspace_bytes < dv.workspace) return LITE_ERR_INVALID_ARG;
     if (dv.workspace && !device_range_ok(workspace, dv.workspace, pl->device)) return LITE_ERR_INVALID_ARG;
     if (dv.workspace && !apart(workspace, dv.workspace, o.ptr, rows_bytes(o, pl->Hq, pl->d))) return LITE_ERR_INVALID_ARG;
