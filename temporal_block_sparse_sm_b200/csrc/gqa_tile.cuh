@@ -135,18 +135,6 @@ __device__ __forceinline__ void mma_ts_block4(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
-// Maxima that keep a NaN.
-__device__ __forceinline__ float max2_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 template <int D, bool F16>
 __global__ void __launch_bounds__(TileCfg<D, F16>::NTHREADS, 1)
 gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -560,14 +548,14 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 float mx[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = max3_nan(__uint_as_float(sc[0][j]), __uint_as_float(sc[0][8 + j]), __uint_as_float(sc[0][16 + j]));
+                for (int j = 0; j < 8; ++j) mx[j] = ptx::max3(__uint_as_float(sc[0][j]), __uint_as_float(sc[0][8 + j]), __uint_as_float(sc[0][16 + j]));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = max3_nan(mx[j], __uint_as_float(sc[0][24 + j]), __uint_as_float(sc[1][j]));
+                for (int j = 0; j < 8; ++j) mx[j] = ptx::max3(mx[j], __uint_as_float(sc[0][24 + j]), __uint_as_float(sc[1][j]));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = max3_nan(mx[j], __uint_as_float(sc[1][8 + j]), __uint_as_float(sc[1][16 + j]));
+                for (int j = 0; j < 8; ++j) mx[j] = ptx::max3(mx[j], __uint_as_float(sc[1][8 + j]), __uint_as_float(sc[1][16 + j]));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = max2_nan(mx[j], __uint_as_float(sc[1][24 + j]));
-                const float m_loc = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]), max2_nan(mx[6], mx[7]));
+                for (int j = 0; j < 8; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(sc[1][24 + j]));
+                const float m_loc = ptx::max3(ptx::max3(mx[0], mx[1], mx[2]), ptx::max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
                 float alpha = 1.0f;
                 bool rescale = false;
                 if (m_loc - m_ref > resc) {              // also the row's first finite maximum
@@ -576,8 +564,6 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     l *= alpha;
                     m_ref = m_loc;
                 }
-                // a visible logit of +inf or NaN leaves the row without a softmax (inf - inf)
-                if (!(m_loc < INFINITY)) l = __uint_as_float(0x7FC00000u);
                 if (__any_sync(0xFFFFFFFFu, rescale) && ok && u > 0) {
                     // the last step's P V may still run (this S only says that the one before it is
                     // done); the next is issued when this step's P is handed over
@@ -604,15 +590,23 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const float neg = (m_ref == -INFINITY ? 0.0f : -m_ref * cl2) + weight_bias<F16>();
                 const uint64_t n2 = ptx::f2(neg, neg);
                 uint64_t acc[4] = {};
+                // a visible logit of +inf or NaN gives a NaN weight (inf - inf), and so a NaN sum and row
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x0, x1;
+                        ptx::f2_split(ptx::fma2(ptx::f2(__uint_as_float(sc[ch][2 * i]), __uint_as_float(sc[ch][2 * i + 1])), c2, n2), x0, x1);
+                        sc[ch][2 * i] = __float_as_uint(x0), sc[ch][2 * i + 1] = __float_as_uint(x1);
+                    }
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sc[ch][i] = __float_as_uint(ptx::ex2(__uint_as_float(sc[ch][i])));
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float x0, x1, p0, p1;
-                        ptx::f2_split(ptx::fma2(ptx::f2(__uint_as_float(sc[ch][2 * i]), __uint_as_float(sc[ch][2 * i + 1])), c2, n2), x0, x1);
-                        p0 = ptx::ex2(x0);
-                        p1 = ptx::ex2(x1);
+                        const float p0 = __uint_as_float(sc[ch][2 * i]), p1 = __uint_as_float(sc[ch][2 * i + 1]);
                         pk[i] = pack16<F16>(p0, p1);
                         acc[i & 3] = ptx::add2(acc[i & 3], ptx::f2(p0, p1));
                     }
