@@ -187,7 +187,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 w.valid = more ? 1 : 0;
                 if (more) {
                     w.q0 = it.s.q0, w.n = it.s.n, w.m = it.s.m, w.i = it.i, w.h = it.h, w.t0 = walk.t0, w.t1 = walk.t1;
-                    w.lim_lo = visible_keys(p.b, it.s, static_cast<int>(static_cast<int64_t>(it.i) * C::ROWS / G));
+                    w.lim_lo = visible_keys(p.b, it.s, static_cast<int>(quotient(static_cast<int64_t>(it.i) * C::ROWS, G)));
                     w.lim_hi = it.keys, w.whole = walk.whole ? 1 : 0, w.slot = walk.slot;
                 }
                 ptx::mbar_arrive(w_full(at));
@@ -236,7 +236,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     for (int r = 0; r < 2; ++r) {
         const int row = gid + 8 * r;
         const bool ok = row < nrows;
-        const int t = ok ? static_cast<int>((row0 + row) / G) : 0, g = ok ? static_cast<int>((row0 + row) % G) : 0;
+        const int t = ok ? static_cast<int>(quotient(row0 + row, G)) : 0, g = ok ? static_cast<int>(row0 + row - static_cast<int64_t>(t) * G) : 0;
         lim[r] = ok ? visible_keys(p.b, seq, t) : 0;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (static_cast<int64_t>(w.q0) + t) * p.q_st +
                                                                  (static_cast<int64_t>(w.h) * G + g) * p.q_sh);
@@ -401,7 +401,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const float mj = s_ml[j][row][0];
         sum += s_ml[j][row][1] * (mj == -INFINITY ? 0.0f : ptx::ex2((mj - mx) * cl2));   // 0 * NaN stays NaN
     }
-    const int t = static_cast<int>((row0 + row) / G), g = static_cast<int>((row0 + row) % G);
+    const int t = static_cast<int>(quotient(row0 + row, G)), g = static_cast<int>(row0 + row - static_cast<int64_t>(t) * G);
     // a row that sees no key is zero; one whose visible logits are all -inf is 0 / 0
     const float inv = visible_keys(p.b, seq, t) == 0 ? 0.0f : 1.0f / sum;
     uint16_t *dst = p.o + (static_cast<int64_t>(w.q0) + t) * p.o_st + (static_cast<int64_t>(w.h) * G + g) * p.o_sh + col;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams 
             t = tl < slot_tokens ? static_cast<int64_t>(it.i) * 2 * slot_tokens + (row >> 7) * slot_tokens + tl : it.n;
         } else {
             const int64_t flat = static_cast<int64_t>(it.i) * rows + row;
-            t = flat / G, g = static_cast<int>(flat % G);
+            t = quotient(flat, G), g = static_cast<int>(flat - t * G);
         }
         float a[CPT] = {}, sum = 0.0f, mx = -INFINITY;
         if (t < it.n) {

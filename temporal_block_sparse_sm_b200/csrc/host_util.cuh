@@ -66,11 +66,11 @@ inline bool fault(const char *what) {
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-using AddrRangeFn = CUresult (*)(CUdeviceptr *, size_t *, CUdeviceptr);
+using PtrAttrsFn = CUresult (*)(unsigned int, CUpointer_attribute *, void **, CUdeviceptr);
 
 struct DriverFns {
     EncodeTiledFn encode = nullptr;
-    AddrRangeFn addr_range = nullptr;
+    PtrAttrsFn ptr_attrs = nullptr;
     bool ok = false;
 };
 
@@ -83,10 +83,10 @@ inline const DriverFns &driver() {
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p1, cudaEnableDefault, &q1) == cudaSuccess &&
             q1 == cudaDriverEntryPointSuccess)
             fns.encode = reinterpret_cast<EncodeTiledFn>(p1);
-        if (cudaGetDriverEntryPoint("cuMemGetAddressRange", &p2, cudaEnableDefault, &q2) == cudaSuccess &&
+        if (cudaGetDriverEntryPoint("cuPointerGetAttributes", &p2, cudaEnableDefault, &q2) == cudaSuccess &&
             q2 == cudaDriverEntryPointSuccess)
-            fns.addr_range = reinterpret_cast<AddrRangeFn>(p2);
-        fns.ok = fns.encode && fns.addr_range;
+            fns.ptr_attrs = reinterpret_cast<PtrAttrsFn>(p2);
+        fns.ok = fns.encode && fns.ptr_attrs;
     });
     return fns;
 }
@@ -95,19 +95,19 @@ inline int cuda_err(cudaError_t e) { return e == cudaSuccess ? LITE_OK : LITE_ER
 
 // Checks that [ptr, ptr + bytes) is device memory of `device` inside one allocation,
 // and that ptr is aligned to `align` bytes (a power of two).
+// One driver call (a serving step asks a dozen times).
 inline bool device_range_ok(const void *ptr, size_t bytes, int device, uintptr_t align = 16) {
     if (!ptr || (reinterpret_cast<uintptr_t>(ptr) & (align - 1u))) return false;
-    cudaPointerAttributes attr;
-    if (cudaPointerGetAttributes(&attr, ptr) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) return false;
-    if (attr.type == cudaMemoryTypeDevice && attr.device != device) return false;
-    CUdeviceptr basep = 0;
+    unsigned int type = 0, managed = 0;
+    int ordinal = -1;
+    CUdeviceptr start = 0;
     size_t size = 0;
-    if (driver().addr_range(&basep, &size, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS) return false;
-    const uintptr_t b = static_cast<uintptr_t>(basep), x = reinterpret_cast<uintptr_t>(ptr);
+    CUpointer_attribute which[5] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                    CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+    void *out[5] = {&type, &managed, &ordinal, &start, &size};
+    if (driver().ptr_attrs(5, which, out, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS) return false;
+    if (!managed && (type != CU_MEMORYTYPE_DEVICE || ordinal != device)) return false;
+    const uintptr_t b = static_cast<uintptr_t>(start), x = reinterpret_cast<uintptr_t>(ptr);
     return x >= b && x - b + bytes <= size;
 }
 

@@ -150,7 +150,7 @@ struct Division {
 };
 // In keys, measured: the turn from one item to the next, and what partial outputs and their join cost.
 constexpr int kTileItemCost = 256, kTileJoinCost = 1280, kTileMinStretch = 512;
-constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 256;
+constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 128;
 constexpr int kManyItems = 8;   // items per block from which whole items come out even
 
 Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_new, int64_t max_keys) {

@@ -82,9 +82,15 @@ __device__ __forceinline__ SeqInfo seq_info(const GqaBatch &p, int b) {
     return s;
 }
 
+// a / b for a, b >= 0; in 32 bits where they fit (a 64-bit division takes about 100 instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 __device__ __forceinline__ int seq_blocks(const GqaBatch &p, int n) {
-    if (p.unit_rows) return static_cast<int>((static_cast<int64_t>(n) * p.G + p.unit_rows - 1) / p.unit_rows);
-    return (n + p.unit_tokens - 1) / p.unit_tokens;
+    return p.unit_rows ? static_cast<int>(quotient(static_cast<int64_t>(n) * p.G + p.unit_rows - 1, p.unit_rows))
+                       : (n + p.unit_tokens - 1) / p.unit_tokens;
 }
 
 // Keys that query token t of a sequence sees (0: none).
@@ -94,15 +100,9 @@ __device__ __forceinline__ int visible_keys(const GqaBatch &p, const SeqInfo &s,
     return v < 0 ? 0 : v;
 }
 
-// a / b for a, b >= 0; in 32 bits where they fit (a 64-bit division takes about 100 instructions).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 // Keys that the last row of block i sees.
 __device__ __forceinline__ int block_keys(const GqaBatch &p, const SeqInfo &s, int i) {
-    const int last = p.unit_rows ? static_cast<int>((min(static_cast<int64_t>(i + 1) * p.unit_rows, static_cast<int64_t>(s.n) * p.G) - 1) / p.G)
+    const int last = p.unit_rows ? static_cast<int>(quotient(min(static_cast<int64_t>(i + 1) * p.unit_rows, static_cast<int64_t>(s.n) * p.G) - 1, p.G))
                                  : min((i + 1) * p.unit_tokens, s.n) - 1;
     return visible_keys(p, s, last);
 }
@@ -130,40 +130,44 @@ struct ScanScratch {
     int items[32], longest[32];
 };
 
-// Units of a block's stretch, 0: items are dealt out whole.  The same in every block (of NT threads).
-template <int NT>
-__device__ __forceinline__ int64_t stretch_units(const GqaBatch &p, int blocks, ScanScratch &sc) {
-    if (!p.may_split) return 0;
-    constexpr int NW = NT / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t units = 0;
-    int items = 0, longest = 0, shortest = 0;
-    for (int b = p.B == 1 ? 0 : threadIdx.x; b < p.B; b += NT) {
-        const SeqInfo s = seq_info(p, b);
-        const int nb = seq_blocks(p, s.n);
-        units += p.Hk * group_units(p, s, nb, nb);
-        items += p.Hk * nb;
-        if (nb > 0) longest = max(longest, s.m), shortest = block_keys(p, s, 0);
-    }
-    if (p.B > 1) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            units += __shfl_xor_sync(0xFFFFFFFFu, units, o);
-            items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
-            longest = max(longest, __shfl_xor_sync(0xFFFFFFFFu, longest, o));
-        }
-        if (lane == 0) sc.sum[warp] = units, sc.items[warp] = items, sc.longest[warp] = longest;
-        __syncthreads();
-        units = 0, items = 0, longest = 0;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) units += sc.sum[k], items += sc.items[k], longest = max(longest, sc.longest[k]);
-    }
+// Units of a block's stretch, 0: items are dealt out whole.  From the batch's units, its items, and
+// the keys of its longest and (of a single sequence) shortest item.
+__device__ __forceinline__ int64_t choose_stretch(const GqaBatch &p, int blocks, int64_t units, int items, int longest, int shortest) {
     const int64_t even = max(quotient(units + blocks - 1, blocks), static_cast<int64_t>(p.min_stretch));
     // Dealt out whole, one sequence's items fall off in length to the shortest, and the blocks end
     // within one of those of each other; those of several sequences within about half the longest.
     const int64_t rounds = (items + blocks - 1) / blocks, most = static_cast<int64_t>(longest) + p.item_cost;
     const int64_t whole = max(most, min(rounds * most, even + (p.B == 1 ? static_cast<int64_t>(shortest) : most / 2)));
     return even + p.join_cost < whole ? even : 0;
+}
+// The same in every block, of NT threads; batches of more than 32 sequences (a warp takes fewer by
+// itself, BlockWalk).
+template <int NT>
+__device__ __forceinline__ int64_t stretch_units(const GqaBatch &p, int blocks, ScanScratch &sc) {
+    if (!p.may_split || p.B <= 32) return 0;
+    constexpr int NW = NT / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t units = 0;
+    int items = 0, longest = 0;
+    for (int b = threadIdx.x; b < p.B; b += NT) {
+        const SeqInfo s = seq_info(p, b);
+        const int nb = seq_blocks(p, s.n);
+        units += p.Hk * group_units(p, s, nb, nb);
+        items += p.Hk * nb;
+        if (nb > 0) longest = max(longest, s.m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        units += __shfl_xor_sync(0xFFFFFFFFu, units, o);
+        items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
+        longest = max(longest, __shfl_xor_sync(0xFFFFFFFFu, longest, o));
+    }
+    if (lane == 0) sc.sum[warp] = units, sc.items[warp] = items, sc.longest[warp] = longest;
+    __syncthreads();
+    units = 0, items = 0, longest = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) units += sc.sum[k], items += sc.items[k], longest = max(longest, sc.longest[k]);
+    return choose_stretch(p, blocks, units, items, longest, 0);
 }
 
 // An item: its sequence, block of rows and head, the keys that its last row sees, and its stretch
@@ -225,28 +229,45 @@ struct WorkCursor {
     int64_t base, total;   // items or units before the 32 sequences, and in them
     SeqInfo s;
     int64_t lo, cnt;       // this lane's sequence: first item or unit, how many
-    __device__ __forceinline__ void load(const GqaBatch &p, bool line, int lane) {
-        const int b = b0 + lane;
-        s = SeqInfo{0, 0, 0, 0};
-        cnt = 0;
-        if (b < p.B) {
-            s = seq_info(p, b);
-            const int nb = seq_blocks(p, s.n);
-            cnt = line ? p.Hk * group_units(p, s, nb, nb) : static_cast<int64_t>(p.Hk) * nb;
-        }
+    __device__ __forceinline__ void fetch(const GqaBatch &p, int lane) {
+        s = b0 + lane < p.B ? seq_info(p, b0 + lane) : SeqInfo{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void count(const GqaBatch &p, bool line) {
+        const int nb = seq_blocks(p, s.n), lane = threadIdx.x & 31;
+        cnt = line ? p.Hk * group_units(p, s, nb, nb) : static_cast<int64_t>(p.Hk) * nb;
         int64_t ci = cnt;
+        if (p.B > 1) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t a = __shfl_up_sync(0xFFFFFFFFu, ci, o);
-            if (lane >= o) ci += a;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t a = __shfl_up_sync(0xFFFFFFFFu, ci, o);
+                if (lane >= o) ci += a;
+            }
         }
         lo = base + ci - cnt;
-        total = __shfl_sync(0xFFFFFFFFu, ci, 31);
+        total = __shfl_sync(0xFFFFFFFFu, ci, p.B > 1 ? 31 : 0);
     }
-    __device__ __forceinline__ void start(const GqaBatch &p, bool line, int lane) {
+    // `stretch`: of stretch_units for more than 32 sequences; else found here, from the one look at them
+    __device__ __forceinline__ void start(const GqaBatch &p, int lane, int64_t &stretch) {
         b0 = 0;
         base = 0;
-        load(p, line, lane);
+        fetch(p, lane);
+        if (p.may_split && p.B <= 32) {
+            const int nb = seq_blocks(p, s.n);
+            int64_t units = p.Hk * group_units(p, s, nb, nb);
+            int items = p.Hk * nb, longest = nb > 0 ? s.m : 0, shortest = 0;
+            if (p.B == 1) {
+                if (nb > 0) shortest = block_keys(p, s, 0);
+                units = __shfl_sync(0xFFFFFFFFu, units, 0), items = __shfl_sync(0xFFFFFFFFu, items, 0);
+                longest = __shfl_sync(0xFFFFFFFFu, longest, 0), shortest = __shfl_sync(0xFFFFFFFFu, shortest, 0);
+            } else {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xFFFFFFFFu, units, o);
+                items = __reduce_add_sync(0xFFFFFFFFu, items);
+                longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+            }
+            stretch = choose_stretch(p, static_cast<int>(gridDim.x), units, items, longest, shortest);
+        }
+        count(p, stretch > 0);
     }
     // the sequence that holds item or unit x (not below an earlier x); false: behind the last
     __device__ __forceinline__ bool find(const GqaBatch &p, bool line, int lane, int64_t x, int &b, SeqInfo &q, int64_t &first) {
@@ -254,7 +275,8 @@ struct WorkCursor {
             if (b0 + 32 >= p.B) return false;
             b0 += 32;
             base += total;
-            load(p, line, lane);
+            fetch(p, lane);
+            count(p, line);
         }
         const int src = __ffs(__ballot_sync(0xFFFFFFFFu, x >= lo && x < lo + cnt)) - 1;
         q.q0 = __shfl_sync(0xFFFFFFFFu, s.q0, src);
@@ -277,7 +299,7 @@ struct BlockWalk {
     __device__ __forceinline__ void start(const GqaBatch &p, int64_t stretch_, JoinItem *joins, int lane) {
         stretch = stretch_;
         if (joins && lane == 0) joins[blockIdx.x] = JoinItem{};
-        cur.start(p, stretch > 0, lane);
+        cur.start(p, lane, stretch);
         x = blockIdx.x * stretch;
         x_end = x + stretch;
         any = false;

@@ -55,8 +55,11 @@ class GroupedPlan:
             raise ValueError("dtype must be torch.bfloat16 or torch.float16")
         self.Hq, self.Hk, self.d, self.dtype = int(Hq), int(Hk), int(d), dtype
         self.device = _c._current_device()
-        self._empty, self._u8, self._i32 = torch.empty, torch.uint8, torch.int32
+        self._torch, self._u8, self._i32, self._f32 = torch, torch.uint8, torch.int32, torch.float32
         self._dev = torch.device("cuda", self.device) if self.device is not None else None
+        # the current stream's handle, without the stream object where torch offers that
+        self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
         self._ws = {}   # workspace bytes by (B, tokens, max_new, max_keys)
         self.handle = _c.lite_attn_gqa_create(self.Hq, self.Hk, self.d,
                                               _c.LITE_DTYPE_BF16 if dtype == torch.bfloat16 else _c.LITE_DTYPE_FP16)
@@ -64,29 +67,29 @@ class GroupedPlan:
         self._fn = lib.lite_attn_prompt, lib.lite_attn_cache_append, lib.lite_attn_cache_attend
 
     # ------------------------------------------------------------ arguments
+    # (the library checks addresses and strides; these look at what it cannot see)
     def _stream(self, stream) -> int:
         if stream is None:
-            import torch
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return self._current(self.device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _rows(self, t, heads: int, name: str):
         """(address, tokens, token stride, head stride) of a [tokens, heads, d] tensor."""
-        if t.dtype is not self.dtype or not t.is_cuda or t.dim() != 3:
+        if t.dtype is not self.dtype or t.dim() != 3:
             raise ValueError(f"{name} must be a CUDA tensor [tokens, {heads}, {self.d}] of {self.dtype}")
         n, h, d = t.shape
         st, sh, sd = t.stride()
         if h != heads or d != self.d or (sd != 1 and n):
             raise ValueError(f"{name} must be [tokens, {heads}, {self.d}] with contiguous rows of d")
         if h == 1:
-            sh = self.d
-        if n == 1:
-            st = max(st, h * self.d)
+            sh = d
+        if n == 1 and st < h * d:
+            st = h * d
         return t.data_ptr(), n, st, sh
 
-    def _ints(self, t, shape, name: str) -> int:
-        if t.dtype is not self._i32 or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
-            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {tuple(shape)}")
+    def _ints(self, t, n: int, name: str) -> int:
+        if t.dtype is not self._i32 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of {n} elements")
         return t.data_ptr()
 
     def _workspace(self, B: int, tokens: int, max_new: int, max_keys: int, stream: int):
@@ -100,11 +103,11 @@ class GroupedPlan:
             return None
         # from the caching allocator, on the call's own stream: reused in that stream's order, and a
         # captured graph's workspace is the graph's own
-        import torch
-        if stream == torch.cuda.current_stream(self.device).cuda_stream:
-            return self._empty(n, dtype=self._u8, device=self._dev)
+        torch = self._torch
+        if stream == self._current(self.device):
+            return torch.empty(n, dtype=self._u8, device=self._dev)
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self._dev)):
-            return self._empty(n, dtype=self._u8, device=self._dev)
+            return torch.empty(n, dtype=self._u8, device=self._dev)
 
     def _scale(self, scale: Optional[float]) -> float:
         return 1.0 / math.sqrt(self.d) if scale is None else float(scale)
@@ -119,10 +122,10 @@ class GroupedPlan:
         rq, ro = self._rows(q, self.Hq, "q"), self._rows(o, self.Hq, "o")
         rk, rv = self._rows(k, self.Hk, "k"), self._rows(v, self.Hk, "v")
         cu_k = cu_q if cu_k is None else cu_k
-        B = cu_q.shape[0] - 1
+        B = cu_q.numel() - 1
         s = self._stream(stream)
         w = self._workspace(B, rq[1], rq[1], rk[1], s)
-        args = _PROMPT.pack(*rq, *ro, *rk, *rv, self._ints(cu_q, (B + 1,), "cu_q"), self._ints(cu_k, (B + 1,), "cu_k"),
+        args = _PROMPT.pack(*rq, *ro, *rk, *rv, self._ints(cu_q, B + 1, "cu_q"), self._ints(cu_k, B + 1, "cu_k"),
                             w.data_ptr() if w is not None else 0, w.shape[0] if w is not None else 0, B,
                             1 if causal else 0, self._scale(scale), 0)
         _c._check(self._fn[0](self.handle, args, s), "lite_attn_prompt")
@@ -185,22 +188,22 @@ class PagedCache:
         rq, ro = (p._rows(q, p.Hq, "q"), p._rows(q_out, p.Hq, "q_out")) if q is not None else (_NO_ROWS, _NO_ROWS)
         if (cos is None) != (sin is None) or (cos is None and positions is not None):
             raise ValueError("cos and sin come together, positions with them")
-        a = (0, 0, 0)
-        rot = 0
+        a, rot = (0, 0, 0), 0
         if cos is not None:
-            for t, nm in ((cos, "cos"), (sin, "sin")):
-                if not t.is_cuda or str(t.dtype) != "torch.float32" or t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
-                    raise ValueError(f"{nm} must be a contiguous CUDA float32 tensor [rows, rot / 2]")
-            rot = 2 * cos.shape[1]
+            f32 = p._f32
+            if cos.dtype is not f32 or sin.dtype is not f32 or cos.dim() != 2 or sin.shape != cos.shape or not (
+                    cos.is_contiguous() and sin.is_contiguous()):
+                raise ValueError("cos and sin must be contiguous CUDA float32 tensors [rows, rot / 2]")
+            rows, half = cos.shape
+            rot = 2 * half
             if rot % 16 or not 16 <= rot <= p.d:
                 raise ValueError("rot must be a multiple of 16, at most d")
-            a = (cos.data_ptr(), sin.data_ptr(), cos.shape[0])
-        B = cu_new.shape[0] - 1
+            a = (cos.data_ptr(), sin.data_ptr(), rows)
+        B, width = cu_new.numel() - 1, table.shape[-1]
         args = _APPEND.pack(*rq, *ro, *rk, *rv, *self._pool, *a,
-                            p._ints(positions, (rk[1],), "positions") if positions is not None else 0,
-                            p._ints(cu_new, (B + 1,), "cu_new"), p._ints(lens, (B,), "lens"),
-                            p._ints(table, (B, table.shape[-1]), "table"), B, table.shape[-1], self.page, self._layout,
-                            rot, 1 if interleaved else 0)
+                            p._ints(positions, rk[1], "positions") if positions is not None else 0,
+                            p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),
+                            p._ints(table, B * width, "table"), B, width, self.page, self._layout, rot, 1 if interleaved else 0)
         _c._check(p._fn[1](p.handle, args, p._stream(stream)), "lite_attn_cache_append")
 
     def attend(self, q, o, lens, cu_new, table, max_new: int, causal: bool = True, scale: Optional[float] = None,
@@ -213,11 +216,11 @@ class PagedCache:
         sequence."""
         p = self.plan
         rq, ro = p._rows(q, p.Hq, "q"), p._rows(o, p.Hq, "o")
-        B, width = cu_new.shape[0] - 1, table.shape[-1]
+        B, width = cu_new.numel() - 1, table.shape[-1]
         s = p._stream(stream)
         w = p._workspace(B, rq[1], max_new, width * self.page, s)
-        args = _ATTEND.pack(*rq, *ro, *self._pool, p._ints(cu_new, (B + 1,), "cu_new"), p._ints(lens, (B,), "lens"),
-                            p._ints(table, (B, width), "table"), w.data_ptr() if w is not None else 0,
+        args = _ATTEND.pack(*rq, *ro, *self._pool, p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),
+                            p._ints(table, B * width, "table"), w.data_ptr() if w is not None else 0,
                             w.shape[0] if w is not None else 0, B, width, self.page, self._layout, max_new,
                             1 if causal else 0, p._scale(scale), 0)
         _c._check(p._fn[2](p.handle, args, s), "lite_attn_cache_attend")
