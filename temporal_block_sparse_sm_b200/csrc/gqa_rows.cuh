@@ -318,20 +318,26 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     acc[n][2] *= alpha[1], acc[n][3] *= alpha[1];
                 }
             }
-            // weights, rounded to 16 bits for the product; the sum adds the rounded ones
+            // Weights for the product, each as two 16-bit numbers, the weight rounded towards zero and
+            // what that left over: the kernel is bound by memory, so the second product costs next to
+            // nothing (0 to 1 %), and the weights' rounding, as large as the output's own, is gone.  Both
+            // are positive for a positive weight, so that an infinite value stays one.
             float neg[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) neg[r] = (m_ref[r] == -INFINITY ? 0.0f : -m_ref[r] * cl2) + weight_bias<F16>();
-            uint32_t pf[4];
+            uint32_t pf[4], pl[4];
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float p0 = ptx::ex2(fmaf(sc[nb][2 * r], cl2, neg[r])), p1 = ptx::ex2(fmaf(sc[nb][2 * r + 1], cl2, neg[r]));
-                    pf[nb * 2 + r] = pack16<F16>(p0, p1);
-                    float a = 0.0f, b = 0.0f;
-                    add16x2<F16>(a, b, pf[nb * 2 + r]);
-                    l[r] += a + b;
+                    const int x = nb * 2 + r;
+                    pf[x] = pack16_down<F16>(p0, p1);
+                    float h0, h1;
+                    unpack16<F16>(pf[x], h0, h1);
+                    constexpr float tiny = F16 ? 0x1p-24f : 0x1p-100f;
+                    pl[x] = pack16<F16>(p0 > 0.0f ? fmaxf(p0 - h0, tiny) : 0.0f, p1 > 0.0f ? fmaxf(p1 - h1, tiny) : 0.0f);
+                    l[r] += p0 + p1;
                 }
             if (!scalar) {
                 // matrices of V: (keys 0-7, d n..n+7), (keys 8-15, same d), then the next 8 d
@@ -344,6 +350,8 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     ptx::ldsm4t(rowa + (n >> 2) * C::CHUNK_BYTES + ((c16 ^ (key & 7)) << 4), b0, b1, b2, b3);
                     ptx::mma16816<F16>(acc[2 * n], pf, b0, b1);
                     ptx::mma16816<F16>(acc[2 * n + 1], pf, b2, b3);
+                    ptx::mma16816<F16>(acc[2 * n], pl, b0, b1);
+                    ptx::mma16816<F16>(acc[2 * n + 1], pl, b2, b3);
                 }
             } else {
 #pragma unroll 1
@@ -352,9 +360,10 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     float wt[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        float a = 0.0f, b = 0.0f;
-                        add16x2<F16>(a, b, __shfl_sync(0xFFFFFFFFu, key < 8 ? pf[r] : pf[2 + r], from));
-                        wt[r] = (key & 1) ? b : a;
+                        float a, b, c, d;
+                        unpack16<F16>(__shfl_sync(0xFFFFFFFFu, key < 8 ? pf[r] : pf[2 + r], from), a, b);
+                        unpack16<F16>(__shfl_sync(0xFFFFFFFFu, key < 8 ? pl[r] : pl[2 + r], from), c, d);
+                        wt[r] = (key & 1) ? b + d : a + c;
                     }
                     const bool see0 = kb + key < lim[0], see1 = kb + key < lim[1];
 #pragma unroll

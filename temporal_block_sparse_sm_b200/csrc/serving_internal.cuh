@@ -399,6 +399,13 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return r;
 }
 template <bool F16>
+__device__ __forceinline__ uint32_t pack16_down(float lo, float hi) {   // towards zero
+    uint32_t r;
+    if constexpr (F16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool F16>
 __device__ __forceinline__ void unpack16(uint32_t v, float &lo, float &hi) {
     if constexpr (F16) {
         const __half2 h = *reinterpret_cast<const __half2 *>(&v);
@@ -423,18 +430,4 @@ __device__ __forceinline__ uint32_t fma_zero16(uint32_t v, uint32_t acc) {
     else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0u), "r"(acc));
     return d;
 }
-// lo += low half of v, hi += high half, each exactly as an f32 (mixed-precision add).
-template <bool F16>
-__device__ __forceinline__ void add16x2(float &lo, float &hi, uint32_t v) {
-    if constexpr (F16)
-        asm("{\n\t.reg .b16 l16, h16;\n\t"
-            "mov.b32 {l16, h16}, %2;\n\t"
-            "add.rn.f32.f16 %0, l16, %0;\n\t"
-            "add.rn.f32.f16 %1, h16, %1;\n\t}"
-            : "+f"(lo), "+f"(hi)
-            : "r"(v));
-    else
-        ptx::add_bf16x2(lo, hi, v);
-}
-
 }  // namespace lite
