@@ -41,7 +41,7 @@ struct GqaParams {
 template <int D>
 struct RowsCfg {
     static constexpr int BN = 64;               // keys of a tile
-    static constexpr int ROWS = 16;
+    static constexpr int ROWS = kFewRows;
     static constexpr int NWARP = 4;             // computing warps
     static constexpr int NTHREADS = 32 * (NWARP + 1);
     static constexpr int DCH = D / 64;
@@ -187,7 +187,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 w.valid = more ? 1 : 0;
                 if (more) {
                     w.q0 = it.s.q0, w.n = it.s.n, w.m = it.s.m, w.i = it.i, w.h = it.h, w.t0 = walk.t0, w.t1 = walk.t1;
-                    w.lim_lo = visible_keys(p.b, it.s, static_cast<int>(quotient(static_cast<int64_t>(it.i) * C::ROWS, G)));
+                    w.lim_lo = visible_keys(p.b, it.s, it.i == 0 ? 0 : static_cast<int>(quotient(static_cast<int64_t>(it.i) * C::ROWS, G)));
                     w.lim_hi = it.keys, w.whole = walk.whole ? 1 : 0, w.slot = walk.slot;
                 }
                 ptx::mbar_arrive(w_full(at));

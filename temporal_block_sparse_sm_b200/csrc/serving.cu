@@ -249,7 +249,6 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     b.G = G;
     b.Hk = pl->Hk;
     b.status = pl->status;
-    b.unit_rows = dv.tile ? 0 : dv.rows;
     b.unit_tokens = dv.tile ? 2 * (128 / G) : 0;
     const int tile = dv.tile ? 128 : RowsCfg<128>::BN;
     b.tile_shift = dv.tile ? 7 : 6;

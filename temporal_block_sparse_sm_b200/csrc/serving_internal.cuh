@@ -29,6 +29,8 @@
 
 namespace lite {
 
+constexpr int kFewRows = 16;   // query rows of an item of the rows kernel
+
 enum KvMode { kKvPacked = 0, kKvPagesBhnd = 1, kKvPagesBnhd = 2 };
 
 struct GqaBatch {
@@ -42,8 +44,7 @@ struct GqaBatch {
     int32_t *status;
     int B, G, Hk, causal, mode;
     int table_w, page_shift;
-    int unit_rows;         // query rows (token, head of the group) of a work item, or 0: unit_tokens tokens
-    int unit_tokens;
+    int unit_tokens;       // query tokens of a work item; 0: kFewRows rows (token, head of the group)
     int tile_shift;        // log2 of the keys of a tile
     int may_split;         // items may be cut
     // in keys: what an item costs beside its keys, what partial outputs and their join cost, and
@@ -89,8 +90,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 
 __device__ __forceinline__ int seq_blocks(const GqaBatch &p, int n) {
-    return p.unit_rows ? static_cast<int>(quotient(static_cast<int64_t>(n) * p.G + p.unit_rows - 1, p.unit_rows))
-                       : (n + p.unit_tokens - 1) / p.unit_tokens;
+    return p.unit_tokens ? (n + p.unit_tokens - 1) / p.unit_tokens
+                         : static_cast<int>((static_cast<int64_t>(n) * p.G + kFewRows - 1) / kFewRows);
 }
 
 // Keys that query token t of a sequence sees (0: none).
@@ -102,18 +103,23 @@ __device__ __forceinline__ int visible_keys(const GqaBatch &p, const SeqInfo &s,
 
 // Keys that the last row of block i sees.
 __device__ __forceinline__ int block_keys(const GqaBatch &p, const SeqInfo &s, int i) {
-    const int last = p.unit_rows ? static_cast<int>(quotient(min(static_cast<int64_t>(i + 1) * p.unit_rows, static_cast<int64_t>(s.n) * p.G) - 1, p.G))
-                                 : min((i + 1) * p.unit_tokens, s.n) - 1;
+    int last;
+    if (p.unit_tokens) {
+        last = min((i + 1) * p.unit_tokens, s.n) - 1;
+    } else {
+        const int64_t end = static_cast<int64_t>(i + 1) * kFewRows;
+        last = end >= static_cast<int64_t>(s.n) * p.G ? s.n - 1 : static_cast<int>(quotient(end - 1, p.G));
+    }
     return visible_keys(p, s, last);
 }
 // Units of block i, and of the first k blocks (last rows first) of one head of a sequence.  Blocks
 // of a few rows count all m keys.
 __device__ __forceinline__ int64_t block_units(const GqaBatch &p, const SeqInfo &s, int i) {
-    return static_cast<int64_t>(p.item_cost) + (p.unit_rows ? s.m : block_keys(p, s, i));
+    return static_cast<int64_t>(p.item_cost) + (p.unit_tokens ? block_keys(p, s, i) : s.m);
 }
 __device__ __forceinline__ int64_t group_units(const GqaBatch &p, const SeqInfo &s, int nb, int k) {
     if (k <= 0) return 0;
-    if (!p.causal || p.unit_rows) return static_cast<int64_t>(k) * (static_cast<int64_t>(s.m) + p.item_cost);
+    if (!p.causal || !p.unit_tokens) return static_cast<int64_t>(k) * (static_cast<int64_t>(s.m) + p.item_cost);
     // block nb - 1 sees m keys; block x - 1 < nb - 1 sees m - n + x * unit_tokens, 0 at least
     const int64_t a = static_cast<int64_t>(s.m) - s.n, tb = p.unit_tokens;
     int64_t lo = nb - k + 1;
@@ -177,8 +183,7 @@ struct LineItem {
     int b, i, h, keys;
     int64_t from, to;
 };
-__device__ __forceinline__ void line_item(const GqaBatch &p, int b, const SeqInfo &s, int64_t base, int64_t x, LineItem &it) {
-    const int nb = seq_blocks(p, s.n);
+__device__ __forceinline__ void line_item(const GqaBatch &p, int b, const SeqInfo &s, int nb, int64_t base, int64_t x, LineItem &it) {
     const int64_t at = x - base;
     int lo = 0, hi = nb - 1;            // the last group that starts at or before x
     while (lo < hi) {
@@ -228,12 +233,14 @@ struct WorkCursor {
     int b0;
     int64_t base, total;   // items or units before the 32 sequences, and in them
     SeqInfo s;
-    int64_t lo, cnt;       // this lane's sequence: first item or unit, how many
+    int nb;                // this lane's sequence: its blocks,
+    int64_t lo, cnt;       // first item or unit, how many
     __device__ __forceinline__ void fetch(const GqaBatch &p, int lane) {
         s = b0 + lane < p.B ? seq_info(p, b0 + lane) : SeqInfo{0, 0, 0, 0};
+        nb = seq_blocks(p, s.n);
     }
     __device__ __forceinline__ void count(const GqaBatch &p, bool line) {
-        const int nb = seq_blocks(p, s.n), lane = threadIdx.x & 31;
+        const int lane = threadIdx.x & 31;
         cnt = line ? p.Hk * group_units(p, s, nb, nb) : static_cast<int64_t>(p.Hk) * nb;
         int64_t ci = cnt;
         if (p.B > 1) {
@@ -252,7 +259,6 @@ struct WorkCursor {
         base = 0;
         fetch(p, lane);
         if (p.may_split && p.B <= 32) {
-            const int nb = seq_blocks(p, s.n);
             int64_t units = p.Hk * group_units(p, s, nb, nb);
             int items = p.Hk * nb, longest = nb > 0 ? s.m : 0, shortest = 0;
             if (p.B == 1) {
@@ -270,7 +276,7 @@ struct WorkCursor {
         count(p, stretch > 0);
     }
     // the sequence that holds item or unit x (not below an earlier x); false: behind the last
-    __device__ __forceinline__ bool find(const GqaBatch &p, bool line, int lane, int64_t x, int &b, SeqInfo &q, int64_t &first) {
+    __device__ __forceinline__ bool find(const GqaBatch &p, bool line, int lane, int64_t x, int &b, SeqInfo &q, int &blocks, int64_t &first) {
         while (x >= base + total) {
             if (b0 + 32 >= p.B) return false;
             b0 += 32;
@@ -284,6 +290,7 @@ struct WorkCursor {
         q.m = __shfl_sync(0xFFFFFFFFu, s.m, src);
         q.k0 = __shfl_sync(0xFFFFFFFFu, s.k0, src);
         first = __shfl_sync(0xFFFFFFFFu, lo, src);
+        blocks = __shfl_sync(0xFFFFFFFFu, nb, src);
         b = b0 + src;
         return true;
     }
@@ -319,21 +326,21 @@ struct BlockWalk {
     }
     __device__ __forceinline__ bool next(const GqaBatch &p, JoinItem *joins, int lane) {
         SeqInfo s;
-        int b;
+        int b, nb;
         int64_t first;
         if (stretch == 0) {         // whole items, back and forth over the blocks
             const int grid = static_cast<int>(gridDim.x), blk = static_cast<int>(blockIdx.x);
             const int64_t item = x * grid + ((x & 1) ? grid - 1 - blk : blk);
             ++x;
-            if (!cur.find(p, false, lane, item, b, s, first)) return false;
+            if (!cur.find(p, false, lane, item, b, s, nb, first)) return false;
             const int y = static_cast<int>(item - first);
-            it.s = s, it.b = b, it.h = y % p.Hk, it.i = seq_blocks(p, s.n) - 1 - y / p.Hk;
+            it.s = s, it.b = b, it.h = y % p.Hk, it.i = nb - 1 - y / p.Hk;
             it.keys = block_keys(p, s, it.i);
             t0 = 0, t1 = tiles_of(p, it.keys), slot = 0, whole = true;
             return true;
         }
-        while (x < x_end && cur.find(p, true, lane, x, b, s, first)) {
-            line_item(p, b, s, first, x, it);
+        while (x < x_end && cur.find(p, true, lane, x, b, s, nb, first)) {
+            line_item(p, b, s, nb, first, x, it);
             const bool mine = line_tiles(p, it, stretch, blockIdx.x, t0, t1, whole);
             slot = line_slot(it, stretch, blockIdx.x);
             x = it.to;
