@@ -378,10 +378,17 @@ int lite_attn_compact_noalloc(const uint32_t *bits, int B, int H, int N, int Br,
  * - What the kernels find wrong in device data (lengths outside the tensors,
  *   a page that does not exist, an angle row out of range) is not used as an
  *   address: the sequence or token is left out and the plan's status becomes
- *   LITE_ERR_DEVICE_CHECK (sticky; lite_attn_gqa_status).
- * - Logits, softmax statistics and output sums are held in 32 bits; the
- *   weights are rounded to the tensors' type for the product with the values
- *   and the output is rounded once.  Results are the same on every run. */
+ *   LITE_ERR_DEVICE_CHECK (sticky; lite_attn_gqa_status).  Lengths, offsets
+ *   and tables must not be written while a call that reads them runs: results
+ *   are undefined then (every access stays inside the tensors even so).
+ * - Logits, softmax statistics and output sums are held in 32 bits and the
+ *   output is rounded once.  For the product with the values the weights are
+ *   rounded to the tensors' type, or, with few query rows, held as two numbers
+ *   of it.  Results are the same on every run.  `scale` times a logit must fit
+ *   32 bits (3.4e38).
+ * - An output's rows (o, q_out) must not overlap: its tokens lie behind one
+ *   another (stride_token >= (heads - 1) * stride_head + d), or its heads do
+ *   (stride_head >= (tokens - 1) * stride_token + d). */
 typedef struct lite_attn_gqa *lite_attn_gqa_t;
 
 #define LITE_DTYPE_BF16 0
@@ -457,7 +464,7 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *args,
  *   scale    : factor of the logits, > 0 (1 / sqrt(d) usually).
  *   workspace: device scratch of lite_attn_gqa_workspace bytes, 16-byte
  *              aligned; free for reuse in stream order.
- * Errors: INVALID_ARG, UNSUPPORTED (2^31 keys or query rows), CUDA; on the
+ * Errors: INVALID_ARG, UNSUPPORTED (over 2^30 keys, 2^31 query rows), CUDA; on the
  * device: LITE_ERR_DEVICE_CHECK, LITE_ERR_DEVICE_TIMEOUT. */
 typedef struct {
     lite_attn_rows_t q, o;

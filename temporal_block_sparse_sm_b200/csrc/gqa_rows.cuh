@@ -36,6 +36,7 @@ struct GqaParams {
     float *ws_o;                      // workspace: [slot][rows of an item][D] unnormalised outputs
     float *ws_ml;                     // [slot][rows of an item][2]: running maximum (raw logit), sum
     JoinItem *joins;                  // [blocks]; null: no item is cut
+    int probe_wait;                   // test of the timeout path: a warp of block 0 waits for what never comes
 };
 
 template <int D>
@@ -137,7 +138,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     using C = RowsCfg<D>;
     constexpr int BN = C::BN, NST = C::NST, DCH = C::DCH, NWORK = 2;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * NST + 2 * NWORK];
+    __shared__ __align__(8) uint64_t bars[2 * NST + 2 * NWORK + 1];
     __shared__ ScanScratch scan;
     __shared__ RowsWork works[NWORK];
     __shared__ float s_ml[C::NWARP][C::ROWS][2];
@@ -162,6 +163,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             ptx::mbar_init(w_full(k), 1);
             ptx::mbar_init(w_empty(k), C::NWARP);
         }
+        ptx::mbar_init(ptx::smem_u32(bars + 2 * NST + 2 * NWORK), 1);   // nothing arrives here
         s_abort = 0u;
         ptx::fence_barrier_init();
     }
@@ -215,9 +217,11 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
 
     // ---------------------------------------------------------------- computing warps
+    if (p.probe_wait && blockIdx.x == 0 && warp == 0) wait_phase_warp(ptx::smem_u32(bars + 2 * NST + 2 * NWORK), 0, wctx);
     const int gid = lane >> 2, tig = lane & 3;
     const float cl2 = p.scale_log2;
-    const float resc = 8.0f / cl2;    // the reference moves when the maximum rose by over 2^8 in weight
+    const float resc = fminf(8.0f / cl2, 3e38f);    // (finite: a first maximum always moves it)
+    // the reference moves when the maximum rose by over 2^8 in weight
     int kv = 0;
     for (int k = 0;; ++k) {
     // one decision for the four warps, so that their barriers stay balanced

@@ -57,7 +57,7 @@ struct TileCfg {
     static constexpr uint32_t OUT_OFF = V_OFF + NST * KV_BYTES, OUT_WARP = 32u * 64u;   // a softmax warp's rows on their way out
     static constexpr uint32_t SMEM_BYTES = OUT_OFF + NSOFT * OUT_WARP + 1024u;
     static constexpr int NWORK = 4;                             // items known ahead
-    static constexpr int NBAR = 6 * NST + 11 * NSLOT + 2 * NWORK;
+    static constexpr int NBAR = 6 * NST + 11 * NSLOT + 2 * NWORK + 1;
     static constexpr uint32_t TMEM_COLS = 512;
     __host__ __device__ static constexpr uint32_t s_col(int s) { return s * 128u; }   // two buffers of BU columns
     __host__ __device__ static constexpr uint32_t o_col(int s) { return 256u + s * static_cast<uint32_t>(D); }
@@ -168,6 +168,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     auto pv_done = [&](int s, int buf) { return slot_bar(9 + buf, s); };
     auto w_full = [&](int k) { return slot_bar(11, 0) + 8u * k; };
     auto w_empty = [&](int k) { return slot_bar(11, 0) + 8u * (NWORK + k); };
+    const uint32_t never = w_empty(NWORK);   // nothing arrives here
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < NST; ++st) {
@@ -194,6 +195,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             ptx::mbar_init(w_full(k), 1);
             ptx::mbar_init(w_empty(k), 4 + C::NSOFT);   // loads, MMA issue (2), cleaning, softmax warps
         }
+        ptx::mbar_init(never, 1);
         s_abort = 0u;
         ptx::fence_barrier_init();
     }
@@ -498,13 +500,15 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     } else {
         // ------------------------------------------------------------ softmax
         ptx::regs_inc<C::REG_SOFTMAX>();
+        if (p.a.probe_wait && blockIdx.x == 0 && warp == 4) wait_all(never, 0);
         const int slot = warp / 4 - 1;
         const int r = (warp & 3) * 32 + lane;
         const int tl = r / pb.G, g = r - tl * pb.G;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t scol = lane_base + C::s_col(slot), ocol = lane_base + C::o_col(slot);
         const float cl2 = p.a.scale_log2;
-        const float resc = 8.0f / cl2;    // the reference moves when the maximum rose by over 2^8 in weight
+        const float resc = fminf(8.0f / cl2, 3e38f);    // (finite: a first maximum always moves it)
+        // the reference moves when the maximum rose by over 2^8 in weight
         const uint64_t c2 = ptx::f2(cl2, cl2);
         uint32_t s_ph = 0u, o_ph = 0u;   // parities: bit buf of s_ph of this buffer's next S (and P V)
         int seq = 0;
@@ -630,10 +634,16 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (!((tw.bad[x >> 7][(x >> 5) & 3] >> (x & 31)) & 1u)) continue;
                     const int key = tw.mask_tile * BN + x;
                     if (key >= limit) continue;
-                    const int64_t from = pb.mode == kKvPacked
-                        ? (tw.k0 + key) * p.v_token
-                        : __ldg(pb.table + static_cast<int64_t>(tw.b) * pb.table_w + (key >> pb.page_shift)) * p.v_page +
-                              (key & ((1 << pb.page_shift) - 1)) * p.v_token;
+                    int64_t from = (tw.k0 + key) * p.v_token;
+                    if (pb.mode != kKvPacked) {
+                        // checked here too: it is the second look, and the table may be written meanwhile by mistake
+                        const int pg = __ldg(pb.table + static_cast<int64_t>(tw.b) * pb.table_w + (key >> pb.page_shift));
+                        if (pg < 0 || pg >= pb.pages) {
+                            atomicExch(pb.status, kStatusCheck);
+                            continue;
+                        }
+                        from = pg * p.v_page + (key & ((1 << pb.page_shift) - 1)) * p.v_token;
+                    }
                     const uint32_t *src = reinterpret_cast<const uint32_t *>(p.v + from + tw.h * p.v_head + ch * 32);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {

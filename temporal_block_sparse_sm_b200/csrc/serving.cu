@@ -44,6 +44,11 @@ bool rows_ok(const lite_attn_rows_t &r, int heads, int d, int device) {
     const size_t elems = static_cast<size_t>(r.tokens - 1) * r.stride_token + static_cast<size_t>(heads - 1) * r.stride_head + d;
     return device_range_ok(r.ptr, elems * 2u, device);
 }
+// An output's rows lie apart: whole tokens behind one another, or whole heads.
+bool rows_apart(const lite_attn_rows_t &r, int heads, int d) {
+    return r.tokens == 0 || r.stride_token >= static_cast<int64_t>(heads - 1) * r.stride_head + d ||
+           r.stride_head >= (r.tokens - 1) * r.stride_token + d;
+}
 size_t rows_bytes(const lite_attn_rows_t &r, int heads, int d) {
     if (r.tokens == 0) return 0;
     return 2u * (static_cast<size_t>(r.tokens - 1) * r.stride_token + static_cast<size_t>(heads - 1) * r.stride_head + d);
@@ -260,6 +265,7 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     std::memset(&t, 0, sizeof t);
     GqaParams &p = t.a;
     p.b = b;
+    p.probe_wait = fault("device_wait") ? 1 : 0;
     p.q = static_cast<const uint16_t *>(q.ptr);
     p.o = static_cast<uint16_t *>(o.ptr);
     p.q_st = q.stride_token, p.q_sh = q.stride_head, p.o_st = o.stride_token, p.o_sh = o.stride_head;
@@ -382,7 +388,7 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *a, vo
     if (rc != LITE_OK) return rc;
     if (a->k.tokens == 0 || a->B == 0) return LITE_OK;
     if (!rows_ok(a->k, plan->Hk, d, dev) || !rows_ok(a->v, plan->Hk, d, dev) ||
-        (has_q && (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->q_out, plan->Hq, d, dev))))
+        (has_q && (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->q_out, plan->Hq, d, dev) || !rows_apart(a->q_out, plan->Hq, d))))
         return LITE_ERR_INVALID_ARG;
     if (!ints_ok(a->cu_new, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->lens, a->B, dev) ||
         !ints_ok(a->table, static_cast<size_t>(a->B) * a->table_width, dev) ||
@@ -455,8 +461,9 @@ int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *a, vo
     if (rc != LITE_OK) return rc;
     if (a->q.tokens == 0 || a->B == 0) return LITE_OK;
     if (a->q.tokens * plan->Hq >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(a->table_width) * a->page >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
-    if (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->o, plan->Hq, d, dev)) return LITE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(a->table_width) * a->page > (int64_t(1) << 30)) return LITE_ERR_UNSUPPORTED;
+    if (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->o, plan->Hq, d, dev) || !rows_apart(a->o, plan->Hq, d))
+        return LITE_ERR_INVALID_ARG;
     if (!ints_ok(a->cu_new, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->lens, a->B, dev) ||
         !ints_ok(a->table, static_cast<size_t>(a->B) * a->table_width, dev))
         return LITE_ERR_INVALID_ARG;
@@ -483,9 +490,9 @@ int lite_attn_prompt(lite_attn_gqa_t plan, const lite_attn_prompt_t *a, void *st
     DeviceScope ds(dev);
     if (!ds.ok) return LITE_ERR_CUDA;
     if (a->q.tokens == 0 || a->B == 0) return LITE_OK;
-    if (a->q.tokens * plan->Hq >= (int64_t(1) << 31)) return LITE_ERR_UNSUPPORTED;
+    if (a->q.tokens * plan->Hq >= (int64_t(1) << 31) || a->k.tokens > (int64_t(1) << 30)) return LITE_ERR_UNSUPPORTED;
     if (!rows_ok(a->q, plan->Hq, d, dev) || !rows_ok(a->o, plan->Hq, d, dev) || !rows_ok(a->k, plan->Hk, d, dev) ||
-        !rows_ok(a->v, plan->Hk, d, dev))
+        !rows_ok(a->v, plan->Hk, d, dev) || !rows_apart(a->o, plan->Hq, d))
         return LITE_ERR_INVALID_ARG;
     if (!ints_ok(a->cu_q, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->cu_k, static_cast<size_t>(a->B) + 1, dev))
         return LITE_ERR_INVALID_ARG;

@@ -320,7 +320,9 @@ struct BlockWalk {
         if (nt == 0 || it.to <= x_end || it.from < x_end - stretch) return;
         const int64_t half = 1 << (p.tile_shift - 1);
         const int64_t q0 = blockIdx.x + (x_end < it.from + half ? 1 : 0);
-        const int64_t q1 = quotient(it.from + (static_cast<int64_t>(nt) << p.tile_shift) - half - 1, stretch);
+        // (no stretch is behind the last block's, unless the lengths are written meanwhile by mistake)
+        const int64_t q1 = min(quotient(it.from + (static_cast<int64_t>(nt) << p.tile_shift) - half - 1, stretch),
+                               static_cast<int64_t>(gridDim.x) - 1);
         if (q0 < q1 && lane == 0)                // else one block writes it
             joins[blockIdx.x] = JoinItem{static_cast<int>(q1 - q0) + 1, line_slot(it, stretch, q0), it.s.q0, it.s.n, it.s.m, it.i, it.h, 0};
     }
@@ -366,6 +368,7 @@ __device__ __forceinline__ bool wait_phase_warp(uint32_t bar, uint32_t parity, c
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
         if (__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(bar, parity))) return true;
+        if (it == 1u && __any_sync(0xFFFFFFFFu, *w.abort_flag != 0u)) return false;   // once given up, quickly through the rest
         if ((it & 63u) == 0u) {
             if (__any_sync(0xFFFFFFFFu, *w.abort_flag != 0u)) return false;
             const uint64_t t = ptx::globaltimer_ns();

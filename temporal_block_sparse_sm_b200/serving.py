@@ -217,6 +217,8 @@ class PagedCache:
         p = self.plan
         rq, ro = p._rows(q, p.Hq, "q"), p._rows(o, p.Hq, "o")
         B, width = cu_new.numel() - 1, table.shape[-1]
+        if max_new > rq[1]:
+            max_new = rq[1]
         s = p._stream(stream)
         w = p._workspace(B, rq[1], max_new, width * self.page, s)
         args = _ATTEND.pack(*rq, *ro, *self._pool, p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),

@@ -552,3 +552,180 @@ def test_plan_of_another_device_than_the_current_one():
     plan.prompt(q, k, v, o2, cu)
     plan.check()
     assert torch.equal(o1, o2) and torch.cuda.current_device() == 0
+
+
+# ---------------------------------------------------------------- failures, graphs, far offsets
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_wait_that_runs_out_ends_the_kernel_and_is_reported(monkeypatch, new):
+    """A warp made to wait on a barrier that nothing arrives on: its bounded wait runs out, the block
+    gives up, the call ends, the plan's status says so, and another plan works on."""
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    g = _gen(41)
+    ks, vs = ([_randn(g, 500, 2, 128, dtype=BF16)] for _ in range(2))
+    kp, vp, table = paged(ks, vs, 16, "bhnd", g)
+    q = _randn(g, new, 8, 128, dtype=BF16)
+    lens, cu = torch.tensor([500], dtype=torch.int32, device="cuda"), offsets([new])
+    plan = serving.GroupedPlan(8, 2, 128)
+    o = torch.empty_like(q)
+    monkeypatch.setenv("LITE_ATTN_FAULT", "device_wait")
+    serving.PagedCache(plan, kp, vp).attend(q, o, lens, cu, table, max_new=new)
+    monkeypatch.delenv("LITE_ATTN_FAULT")
+    with pytest.raises(liteattn.LiteAttnError) as e:
+        plan.check()
+    assert e.value.code == liteattn.LITE_ERR_DEVICE_TIMEOUT
+    other = serving.GroupedPlan(8, 2, 128)
+    serving.PagedCache(other, kp, vp).attend(q, o, lens, cu, table, max_new=new)
+    other.check()
+    want, tol = seq_reference(q, ks[0], vs[0], True, 1 / math.sqrt(128))
+    assert_close(o, want, tol)
+
+
+def test_host_faults_are_reported_without_a_launch(monkeypatch):
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    plan = serving.GroupedPlan(4, 2, 64)
+    z = lambda *s, dt=BF16: torch.zeros(*s, dtype=dt, device="cuda")   # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")   # noqa: E731
+    cache = serving.PagedCache(plan, z(3, 2, 16, 64), z(3, 2, 16, 64))
+    monkeypatch.setenv("LITE_ATTN_FAULT", "launch")
+    n0 = liteattn.lite_attn_launch_count()
+    for call in (lambda: cache.attend(z(2, 4, 64), z(2, 4, 64), i(1), i(2), i(1, 3), max_new=1),
+                 lambda: cache.append(z(2, 2, 64), z(2, 2, 64), i(1), i(2), i(1, 3)),
+                 lambda: plan.prompt(z(2, 4, 64), z(2, 2, 64), z(2, 2, 64), z(2, 4, 64), i(2))):
+        with pytest.raises(liteattn.LiteAttnError) as e:
+            call()
+        assert e.value.code == liteattn.LITE_ERR_CUDA
+    assert liteattn.lite_attn_launch_count() == n0
+    monkeypatch.setenv("LITE_ATTN_FAULT", "status")
+    with pytest.raises(liteattn.LiteAttnError) as e:
+        plan.check()
+    assert e.value.code == liteattn.LITE_ERR_DEVICE_TIMEOUT
+
+
+def test_two_graphs_of_one_plan_replayed_at_the_same_time():
+    """Two captures of one plan, each with a workspace of its own, replayed together on two streams."""
+    from temporal_block_sparse_sm_b200 import serving
+    g = _gen(51)
+    Hq, Hk, d = 8, 2, 128
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    work = []
+    for new, total in (([1, 1], [30000, 7]), ([100, 3], [9000, 5000])):
+        ks, vs = ([_randn(g, m, Hk, d, dtype=BF16) for m in total] for _ in range(2))
+        kp, vp, table = paged(ks, vs, 64, "bhnd", g)
+        q = _randn(g, sum(new), Hq, d, dtype=BF16)
+        lens, cu, o = torch.tensor(total, dtype=torch.int32, device="cuda"), offsets(new), torch.empty_like(q)
+        cache = serving.PagedCache(plan, kp, vp)
+        cache.attend(q, o, lens, cu, table, max_new=max(new))
+        torch.cuda.synchronize()
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            cache.attend(q, o, lens, cu, table, max_new=max(new))
+        work.append((graph, s, o, o.clone(), (ks, vs, kp, vp, table, q, lens, cu, cache)))
+    for _ in range(20):
+        for _, _, o, _, _ in work:
+            o.zero_()
+        torch.cuda.synchronize()
+        for graph, s, *_ in work:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, o, want, _ in work:
+            assert torch.equal(o, want)
+    plan.check()
+
+
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+@pytest.mark.parametrize("new", [1, 30])
+def test_pages_far_into_a_large_pool(layout, new):
+    """A pool of over 2^32 bytes and 2^31 elements, its last pages in use."""
+    from temporal_block_sparse_sm_b200 import serving
+    g = _gen(61)
+    Hq, Hk, d, page = 8, 2, 128, 256
+    pages = (1 << 31) // (page * Hk * d) + 40
+    shape = (pages, Hk, page, d) if layout == "bhnd" else (pages, page, Hk, d)
+    kp, vp = (torch.empty(shape, dtype=BF16, device="cuda") for _ in range(2))
+    m = 3000
+    table = torch.arange(pages - 1, pages - 1 - 12, -1, device="cuda").int().view(1, 12)
+    ks, vs = (_randn(g, m, Hk, d, dtype=BF16) for _ in range(2))
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    cache = serving.PagedCache(plan, kp, vp, layout=layout)
+    lens = torch.tensor([m], dtype=torch.int32, device="cuda")
+    cache.append(ks, vs, lens, offsets([m]), table)
+    q = _randn(g, new, Hq, d, dtype=BF16)
+    o = torch.empty_like(q)
+    cache.attend(q, o, lens, offsets([new]), table, max_new=new)
+    plan.check()
+    want, tol = seq_reference(q, ks, vs, True, 1 / math.sqrt(d))
+    assert_close(o, want, tol)
+
+
+def test_many_splits_of_one_item_and_long_keys():
+    """One key head, few rows, a long cache: one item cut over all blocks, in both kernels."""
+    for new in (1, 4, 5, 64):
+        _attend_case(4, 1, 128, BF16, 64, "bhnd", [new], [40000 + new], seed=new)
+    _attend_case(128, 1, 64, FP16, 16, "bnhd", [1], [30011], seed=9)
+
+
+def test_ragged_batches_of_every_kind():
+    """Random batches over both kernels and both divisions, lengths from nothing to thousands."""
+    import random
+    r = random.Random(7)
+    for k in range(12):
+        Hk = r.choice([1, 2, 3])
+        Hq = Hk * r.choice([1, 2, 5, 8])
+        B = r.choice([1, 2, 7, 33, 40])
+        top = r.choice([1, 3, 60, 300])
+        ctx = r.choice([0, 50, 3000, 9000 if B < 8 else 300])
+        new = [r.randint(0, top) for _ in range(B)]
+        total = [n + r.randint(0, ctx) if r.random() < 0.9 else r.randint(0, n) for n in new]
+        _attend_case(Hq, Hk, r.choice([64, 128]), r.choice([BF16, FP16]), r.choice([16, 64, 512]), r.choice(["bhnd", "bnhd"]), new, total,
+                     causal=r.random() < 0.8, seed=100 + k, pad=r.randint(0, 3), lead=r.randint(0, 3))
+
+
+def test_misaligned_views_are_refused():
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    plan = serving.GroupedPlan(4, 2, 64)
+    base = torch.zeros(5 * 4 * 64 + 8, dtype=BF16, device="cuda")
+    q = base[4:4 + 5 * 256].view(5, 4, 64)        # 8 bytes past a 16-byte boundary
+    k, v, o = (torch.zeros(5, h, 64, dtype=BF16, device="cuda") for h in (2, 2, 4))
+    with pytest.raises(liteattn.LiteAttnError):
+        plan.prompt(q, k, v, o, offsets([5]))
+    with pytest.raises(liteattn.LiteAttnError):
+        plan.prompt(k[:, :1].expand(5, 4, 64), k, v, o, offsets([5]))   # one head four times: overlapping rows
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    plan = serving.GroupedPlan(4, 2, 64)
+    q = torch.zeros(5, 4, 64, dtype=BF16, device="cuda")
+    k, v = (torch.zeros(5, 2, 64, dtype=BF16, device="cuda") for _ in range(2))
+    flat = torch.zeros(4096, dtype=BF16, device="cuda")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")   # noqa: E731
+    cache = serving.PagedCache(plan, *(torch.zeros(3, 2, 16, 64, dtype=BF16, device="cuda") for _ in range(2)))
+    for bad in (flat.as_strided((5, 4, 64), (64, 64, 1)), flat.as_strided((5, 4, 64), (128, 64, 1)), flat.as_strided((5, 4, 64), (64, 256, 1))):
+        for call in (lambda: plan.prompt(q, k, v, bad, offsets([5])),
+                     lambda: cache.attend(q, bad, i(1), i(2), i(1, 3), max_new=1),
+                     lambda: cache.append(k, v, i(1), i(2), i(1, 3), q=q, q_out=bad)):
+            with pytest.raises(liteattn.LiteAttnError) as e:
+                call()
+            assert e.value.code == liteattn.LITE_ERR_INVALID_ARG
+    heads_first = torch.zeros(4, 5, 64, dtype=BF16, device="cuda").transpose(0, 1)
+    plan.prompt(q, k, v, heads_first, offsets([5]))
+    plan.check()
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_the_smallest_and_a_large_scale(new):
+    """A scale so small that every visible key weighs the same, and one that leaves the largest logit."""
+    for scale in (1e-42, 1e-30, 30.0):
+        _attend_case(8, 2, 64, FP16, 16, "bhnd", [new, new], [400, new], scale=scale, seed=new)
+
+
+def test_too_many_keys_are_refused():
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    plan = serving.GroupedPlan(4, 2, 64)
+    cache = serving.PagedCache(plan, *(torch.zeros(1, 2, 65536, 64, dtype=BF16, device="cuda") for _ in range(2)))
+    q = torch.zeros(1, 4, 64, dtype=BF16, device="cuda")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")   # noqa: E731
+    with pytest.raises(liteattn.LiteAttnError) as e:
+        cache.attend(q, torch.zeros_like(q), i(1), i(2), i(1, (1 << 14) + 1), max_new=1)
+    assert e.value.code == liteattn.LITE_ERR_UNSUPPORTED
