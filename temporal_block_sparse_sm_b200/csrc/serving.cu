@@ -154,7 +154,7 @@ struct Division {
     size_t workspace;
 };
 // In keys, measured: the turn from one item to the next, and what partial outputs and their join cost.
-constexpr int kTileItemCost = 256, kTileJoinCost = 1280, kTileMinStretch = 512;
+constexpr int kTileItemCost = 256, kTileJoinCost = 1280, kTileMinStretch = 256;
 constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 128;
 constexpr int kManyItems = 8;   // items per block from which whole items come out even
 
