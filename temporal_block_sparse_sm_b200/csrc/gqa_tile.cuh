@@ -7,7 +7,8 @@
 // A work item is 256 query rows of one key head: two slots of 128 rows, a row being one
 // (token, head of the group) pair, so that the G heads of a group share every key and value
 // that is loaded, and a slot covers 128 / G whole tokens (one TMA box of G heads by that many
-// tokens fills it for any G; rows behind G * (128 / G) hold nothing).  Each slot owns 128
+// tokens fills it for any G; rows behind G * (128 / G) hold nothing).  (In a small batch an
+// item is a single slot, and the second one idle.)  Each slot owns 128
 // TMEM columns of S and D of O; P is written over S and read by the MMA from TMEM.
 //
 // Blocks are persistent, one per SM: segment x of the batch goes to block x mod grid, back
@@ -71,7 +72,7 @@ struct TileCfg {
 // What the roles of a block need to know of one item (shared memory).
 struct TileWork {
     int64_t k0;
-    int q0, n, m, b, h, tok0;
+    int q0, n, m, b, h, tok0, end;   // its tokens [tok0, end) of the sequence's
     int whole, slot;              // all its keys are here: the output is final; else the workspace slot
     int t_lo, n_u, us0, us1;      // first key tile; softmax steps of the segment, and those of each slot
     int lim_lo, lim_hi;           // keys that the first row sees, and the most that any sees
@@ -170,6 +171,11 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     auto w_empty = [&](int k) { return slot_bar(11, 0) + 8u * (NWORK + k); };
     const uint32_t never = w_empty(NWORK);   // nothing arrives here
 
+    if (threadIdx.x == 32) {
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+    }
     if (threadIdx.x == 0) {
         for (int st = 0; st < NST; ++st) {
             ptx::mbar_init(k_full(st), 1);
@@ -226,13 +232,14 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const LineItem &it = walk.it;
                 const int t0 = walk.t0, t1 = walk.t1;
                 int us0 = 0, us1 = 0, v0 = 0, v1 = 0;
-                const int tok0 = more ? it.i * 2 * p.slot_tokens : 0;
+                const int tok0 = more ? it.i * pb.unit_tokens : 0;
+                const int end = min(tok0 + pb.unit_tokens, it.s.n);     // behind the item's last token
                 int lim_lo = 0;
                 if (more) {
                     lim_lo = visible_keys(pb, it.s, tok0);
                     const int key_lo = t0 * BN, key_hi = min(t1 * BN, it.s.m);
                     auto steps_of = [&](int first, int &vis) {
-                        const int last = min(first + p.slot_tokens, it.s.n) - 1;
+                        const int last = min(first + p.slot_tokens, end) - 1;
                         vis = first <= last ? visible_keys(pb, it.s, last) : 0;
                         const int keys = min(vis, key_hi) - key_lo;
                         return keys > 0 ? (keys + C::BU - 1) / C::BU : 0;
@@ -246,7 +253,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (lane == 0) {
                     tw.valid = more ? 1 : 0;
                     if (more) {
-                        tw.k0 = it.s.k0, tw.q0 = it.s.q0, tw.n = it.s.n, tw.m = it.s.m, tw.b = it.b, tw.h = it.h;
+                        tw.k0 = it.s.k0, tw.q0 = it.s.q0, tw.n = it.s.n, tw.m = it.s.m, tw.b = it.b, tw.h = it.h, tw.end = end;
                         tw.tok0 = tok0, tw.whole = walk.whole ? 1 : 0, tw.slot = walk.slot, tw.t_lo = t0;
                         tw.us0 = us0, tw.us1 = us1, tw.n_u = max(us0, us1);
                         tw.lim_lo = lim_lo, tw.lim_hi = max(v0, v1);
@@ -522,7 +529,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             int limit = 0;                // keys that this row sees (0 also for rows that do not exist)
             {
                 const int t = tw.tok0 + slot * p.slot_tokens + tl;
-                if (tl < p.slot_tokens && t < tw.n) limit = pb.causal ? max(0, tw.m - tw.n + t + 1) : tw.m;
+                if (tl < p.slot_tokens && t < tw.end) limit = pb.causal ? max(0, tw.m - tw.n + t + 1) : tw.m;
             }
             const int mine = limit - tw.t_lo * BN;    // of them from the first tile on
             float m_ref = -INFINITY, l = 0.0f;
@@ -627,7 +634,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
             // -------------------------------------------------------- epilogue
             const int t = tw.tok0 + slot * p.slot_tokens + tl;
-            const bool row_valid = tl < p.slot_tokens && t < tw.n;
+            const bool row_valid = tl < p.slot_tokens && t < tw.end;
             auto add_bad = [&](int ch, uint32_t (&o)[32]) {   // values that are not finite, to the rows that see them
 #pragma unroll 1
                 for (int x = 0; x < 512; ++x) {

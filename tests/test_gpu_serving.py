@@ -729,3 +729,15 @@ def test_too_many_keys_are_refused():
     with pytest.raises(liteattn.LiteAttnError) as e:
         cache.attend(q, torch.zeros_like(q), i(1), i(2), i(1, (1 << 14) + 1), max_new=1)
     assert e.value.code == liteattn.LITE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hk,d,dtype,new,total", [
+    (32, 8, 128, BF16, [100] * 20, [600] * 20),         # two slots to an item, whole items, more than one per block
+    (20, 4, 64, FP16, [130, 1, 64, 65] * 12, [200, 1, 64, 900] * 12),
+    (16, 4, 128, BF16, [64], [1000]),                   # one slot to an item
+    (10, 2, 64, BF16, [25, 26, 51, 1], [700, 26, 600, 30]),
+    (5, 1, 128, FP16, [1000], [1000]),
+])
+def test_items_of_one_slot_and_of_two(Hq, Hk, d, dtype, new, total, causal):
+    _attend_case(Hq, Hk, d, dtype, 32, "bhnd", new, total, causal=causal, seed=len(new), pad=3)
