@@ -145,6 +145,9 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     __shared__ __align__(16) float s_o[C::NWARP][C::ROWS][36];   // 32 columns of the warps' outputs at a time
     __shared__ uint32_t s_abort;
 
+    GqaBatch pb = p.b;               // what is fixed for this kernel, as constants
+    pb.unit_tokens = 0, pb.tile_shift = 6;
+    static_assert(BN == 64);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t raw_s = ptx::smem_u32(smem_raw);
     const uint32_t base_s = (raw_s + 1023u) & ~1023u;
@@ -167,20 +170,20 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         s_abort = 0u;
         ptx::fence_barrier_init();
     }
-    const int64_t stretch = stretch_units<C::NTHREADS>(p.b, gridDim.x, scan);
+    const int64_t stretch = stretch_units<C::NTHREADS>(pb, gridDim.x, scan);
     __syncthreads();
     join_may_start();
-    const int G = p.b.G;
-    const WaitScope wctx{&s_abort, p.b.status};
+    const int G = pb.G;
+    const WaitScope wctx{&s_abort, pb.status};
 
     if (warp == C::NWARP) {
         // ------------------------------------------------------------ items and loads
         BlockWalk walk;
-        walk.start(p.b, stretch, p.joins, lane);
+        walk.start(pb, stretch, p.joins, lane);
         int kv = 0;                  // tiles loaded so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            const bool more = walk.next(p.b, p.joins, lane);
+            const bool more = walk.next(pb, p.joins, lane);
             const LineItem &it = walk.it;
             const int at = k % NWORK;
             if (!wait_phase_warp(w_empty(at), ((k / NWORK) & 1) ^ 1u, wctx)) break;
@@ -189,14 +192,14 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 w.valid = more ? 1 : 0;
                 if (more) {
                     w.q0 = it.s.q0, w.n = it.s.n, w.m = it.s.m, w.i = it.i, w.h = it.h, w.t0 = walk.t0, w.t1 = walk.t1;
-                    w.lim_lo = visible_keys(p.b, it.s, it.i == 0 ? 0 : static_cast<int>(quotient(static_cast<int64_t>(it.i) * C::ROWS, G)));
+                    w.lim_lo = visible_keys(pb, it.s, it.i == 0 ? 0 : static_cast<int>(quotient(static_cast<int64_t>(it.i) * C::ROWS, G)));
                     w.lim_hi = it.keys, w.whole = walk.whole ? 1 : 0, w.slot = walk.slot;
                 }
                 ptx::mbar_arrive(w_full(at));
             }
             __syncwarp();
             if (!more) break;
-            KvTiles<BN, DCH> tiles(p.b, it.s.k0, it.b, it.h, it.keys);
+            KvTiles<BN, DCH> tiles(pb, it.s.k0, it.b, it.h, it.keys);
             int pg = walk.t0 < walk.t1 ? tiles.page_of(walk.t0, lane) : -1;
             for (int t = walk.t0; t < walk.t1; ++t, ++kv) {
                 const int st = kv % NST;
@@ -241,7 +244,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int row = gid + 8 * r;
         const bool ok = row < nrows;
         const int t = ok ? static_cast<int>(quotient(row0 + row, G)) : 0, g = ok ? static_cast<int>(row0 + row - static_cast<int64_t>(t) * G) : 0;
-        lim[r] = ok ? visible_keys(p.b, seq, t) : 0;
+        lim[r] = ok ? visible_keys(pb, seq, t) : 0;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (static_cast<int64_t>(w.q0) + t) * p.q_st +
                                                                  (static_cast<int64_t>(w.h) * G + g) * p.q_sh);
 #pragma unroll
@@ -416,7 +419,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     const int t = static_cast<int>(quotient(row0 + row, G)), g = static_cast<int>(row0 + row - static_cast<int64_t>(t) * G);
     // a row that sees no key is zero; one whose visible logits are all -inf is 0 / 0
-    const float inv = visible_keys(p.b, seq, t) == 0 ? 0.0f : 1.0f / sum;
+    const float inv = visible_keys(pb, seq, t) == 0 ? 0.0f : 1.0f / sum;
     uint16_t *dst = p.o + (static_cast<int64_t>(w.q0) + t) * p.o_st + (static_cast<int64_t>(w.h) * G + g) * p.o_sh + col;
     const int64_t ws_at = static_cast<int64_t>(w.slot) * C::ROWS + row;
 #pragma unroll

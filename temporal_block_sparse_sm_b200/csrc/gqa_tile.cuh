@@ -205,7 +205,9 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         s_abort = 0u;
         ptx::fence_barrier_init();
     }
-    const GqaBatch &pb = p.a.b;
+    GqaBatch pb = p.a.b;             // what is fixed for this kernel, as constants
+    pb.tile_shift = 7;
+    static_assert(BN == 128);
     const int64_t stretch = stretch_units<C::NTHREADS>(pb, gridDim.x, scan);
     join_may_start();
     const WaitScope wctx{&s_abort, pb.status};
