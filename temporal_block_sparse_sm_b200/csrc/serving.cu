@@ -157,6 +157,11 @@ struct Division {
 // In keys, measured: the turn from one item to the next, and what partial outputs and their join cost.
 constexpr int kTileItemCost = 256, kTileJoinCost = 1280, kTileMinStretch = 256;
 constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 128;
+// Eighths of a key that a key costs an item whose second slot is empty, measured: 6 at d = 128 (a
+// 1,560-token frame over 32,760 keys of 12 heads, 6.1 items a head: 378 us with 8, 361 with 6, 414
+// with 4), all 8 at d = 64 (880 tokens over 14,000 keys of 24 heads: 141 us with 8 or 6, 160 with
+// 5; 11 chunks of up to 513 tokens: 164 us with 8, 170 with 6).
+constexpr int kTileHalfWeight128 = 6, kTileHalfWeight64 = 8;
 constexpr int kManyItems = 8;   // items per block from which whole items come out even
 
 Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_new, int64_t max_keys) {
@@ -272,6 +277,7 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     b.item_cost = dv.tile ? kTileItemCost : kRowsItemCost;
     b.join_cost = dv.tile ? kTileJoinCost : kRowsJoinCost;
     b.min_stretch = dv.tile ? kTileMinStretch : kRowsMinStretch;
+    b.half_weight = pl->d == 128 ? kTileHalfWeight128 : kTileHalfWeight64;
     TileParams t;
     std::memset(&t, 0, sizeof t);
     GqaParams &p = t.a;

@@ -13,7 +13,8 @@
 // Division among the blocks.  A batch of many items (block of query rows, key head) is dealt
 // out whole, in order of length within a sequence, back and forth over the blocks.  With few
 // items the batch is laid out on a line instead, an item taking as many units as its last row
-// sees keys, and item_cost for its start and end; each block takes an equal stretch of the line,
+// sees keys (half_weight eighths of that where it fills only the first of the tile kernel's two
+// slots), and item_cost for its start and end; each block takes an equal stretch of the line,
 // cut at the nearest tile.  A block then has at most two partial items, at the ends of its
 // stretch: a partial item's unnormalised output, running maximum and sum go to one of the block's
 // two workspace slots, which bounds the workspace whatever the batch, and a second kernel joins
@@ -50,6 +51,7 @@ struct GqaBatch {
     // in keys: what an item costs beside its keys, what partial outputs and their join cost, and
     // the shortest stretch (more than a tile, so that no stretch inside an item is without one)
     int item_cost, join_cost, min_stretch;
+    int half_weight;       // eighths of a key that a key costs an item of no more than half unit_tokens
 };
 
 struct SeqInfo {
@@ -112,21 +114,28 @@ __device__ __forceinline__ int block_keys(const GqaBatch &p, const SeqInfo &s, i
     }
     return visible_keys(p, s, last);
 }
+// Eighths of a unit that a key of block i takes; only a sequence's last block can be half empty.
+__device__ __forceinline__ int block_weight(const GqaBatch &p, const SeqInfo &s, int i) {
+    return p.unit_tokens && 2 * (s.n - i * p.unit_tokens) <= p.unit_tokens ? p.half_weight : 8;
+}
+__device__ __forceinline__ int64_t units_of(int64_t keys, int weight) { return (keys * weight + 7) >> 3; }
 // Units of block i, and of the first k blocks (last rows first) of one head of a sequence.  Blocks
 // of a few rows count all m keys.
-__device__ __forceinline__ int64_t block_units(const GqaBatch &p, const SeqInfo &s, int i) {
-    return static_cast<int64_t>(p.item_cost) + (p.unit_tokens ? block_keys(p, s, i) : s.m);
+__device__ __forceinline__ int64_t block_units(const GqaBatch &p, const SeqInfo &s, int i, int weight) {
+    return static_cast<int64_t>(p.item_cost) + (p.unit_tokens ? units_of(block_keys(p, s, i), weight) : s.m);
 }
 __device__ __forceinline__ int64_t group_units(const GqaBatch &p, const SeqInfo &s, int nb, int k) {
     if (k <= 0) return 0;
-    if (!p.causal || !p.unit_tokens) return static_cast<int64_t>(k) * (static_cast<int64_t>(s.m) + p.item_cost);
+    if (!p.unit_tokens) return static_cast<int64_t>(k) * (static_cast<int64_t>(s.m) + p.item_cost);
+    const int64_t last = units_of(s.m, block_weight(p, s, nb - 1));
+    if (!p.causal) return static_cast<int64_t>(k) * p.item_cost + static_cast<int64_t>(k - 1) * s.m + last;
     // block nb - 1 sees m keys; block x - 1 < nb - 1 sees m - n + x * unit_tokens, 0 at least
     const int64_t a = static_cast<int64_t>(s.m) - s.n, tb = p.unit_tokens;
     int64_t lo = nb - k + 1;
     const int64_t first = a > 0 ? 1 : quotient(-a, tb) + 1;
     lo = lo < first ? first : lo;
     const int64_t hi = nb - 1;
-    int64_t sum = static_cast<int64_t>(k) * p.item_cost + s.m;
+    int64_t sum = static_cast<int64_t>(k) * p.item_cost + last;
     if (lo <= hi) sum += (hi - lo + 1) * a + tb * ((lo + hi) * (hi - lo + 1) / 2);
     return sum;
 }
@@ -136,8 +145,12 @@ struct ScanScratch {
     int items[32], longest[32];
 };
 
+// Units that the longest item of a sequence takes, but for item_cost.
+__device__ __forceinline__ int longest_of(const GqaBatch &p, const SeqInfo &s, int nb) {
+    return nb == 0 ? 0 : nb > 1 ? s.m : static_cast<int>(units_of(s.m, block_weight(p, s, 0)));
+}
 // Units of a block's stretch, 0: items are dealt out whole.  From the batch's units, its items, and
-// the keys of its longest and (of a single sequence) shortest item.
+// the units of its longest and (of a single sequence) shortest item.
 __device__ __forceinline__ int64_t choose_stretch(const GqaBatch &p, int blocks, int64_t units, int items, int longest, int shortest) {
     const int64_t even = max(quotient(units + blocks - 1, blocks), static_cast<int64_t>(p.min_stretch));
     // Dealt out whole, one sequence's items fall off in length to the shortest, and the blocks end
@@ -160,7 +173,7 @@ __device__ __forceinline__ int64_t stretch_units(const GqaBatch &p, int blocks, 
         const int nb = seq_blocks(p, s.n);
         units += p.Hk * group_units(p, s, nb, nb);
         items += p.Hk * nb;
-        if (nb > 0) longest = max(longest, s.m);
+        longest = max(longest, longest_of(p, s, nb));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -180,7 +193,7 @@ __device__ __forceinline__ int64_t stretch_units(const GqaBatch &p, int blocks, 
 // [from, to) of the line.
 struct LineItem {
     SeqInfo s;
-    int b, i, h, keys;
+    int b, i, h, keys, weight;
     int64_t from, to;
 };
 __device__ __forceinline__ void line_item(const GqaBatch &p, int b, const SeqInfo &s, int nb, int64_t base, int64_t x, LineItem &it) {
@@ -195,7 +208,8 @@ __device__ __forceinline__ void line_item(const GqaBatch &p, int b, const SeqInf
     it.b = b;
     it.i = nb - 1 - lo;
     it.keys = block_keys(p, s, it.i);
-    const int64_t start = p.Hk * group_units(p, s, nb, lo), len = block_units(p, s, it.i);
+    it.weight = block_weight(p, s, it.i);
+    const int64_t start = p.Hk * group_units(p, s, nb, lo), len = block_units(p, s, it.i, it.weight);
     it.h = static_cast<int>(quotient(at - start, len));
     it.from = base + start + it.h * len;
     it.to = it.from + len;
@@ -207,7 +221,8 @@ __device__ __forceinline__ int tiles_of(const GqaBatch &p, int keys) {
 __device__ __forceinline__ bool line_tiles(const GqaBatch &p, const LineItem &it, int64_t stretch, int64_t q, int &t0, int &t1, bool &whole) {
     const int nt = tiles_of(p, it.keys);
     auto cut = [&](int64_t x) {          // a boundary at x: the nearest tile
-        const int64_t t = (x - it.from + (1 << (p.tile_shift - 1))) >> p.tile_shift;
+        const int64_t keys = it.weight == 8 ? x - it.from : quotient(8 * (x - it.from), it.weight);
+        const int64_t t = (keys + (1 << (p.tile_shift - 1))) >> p.tile_shift;
         return x <= it.from ? 0 : x >= it.to || t > nt ? nt : static_cast<int>(t);
     };
     t0 = cut(q * stretch);
@@ -260,9 +275,9 @@ struct WorkCursor {
         fetch(p, lane);
         if (p.may_split && p.B <= 32) {
             int64_t units = p.Hk * group_units(p, s, nb, nb);
-            int items = p.Hk * nb, longest = nb > 0 ? s.m : 0, shortest = 0;
+            int items = p.Hk * nb, longest = longest_of(p, s, nb), shortest = 0;
             if (p.B == 1) {
-                if (nb > 0) shortest = block_keys(p, s, 0);
+                if (nb > 0) shortest = min(longest, block_keys(p, s, 0));
                 units = __shfl_sync(0xFFFFFFFFu, units, 0), items = __shfl_sync(0xFFFFFFFFu, items, 0);
                 longest = __shfl_sync(0xFFFFFFFFu, longest, 0), shortest = __shfl_sync(0xFFFFFFFFu, shortest, 0);
             } else {
@@ -319,9 +334,9 @@ struct BlockWalk {
         const int nt = any ? tiles_of(p, it.keys) : 0;
         if (nt == 0 || it.to <= x_end || it.from < x_end - stretch) return;
         const int64_t half = 1 << (p.tile_shift - 1);
-        const int64_t q0 = blockIdx.x + (x_end < it.from + half ? 1 : 0);
+        const int64_t q0 = blockIdx.x + (x_end < it.from + units_of(half, it.weight) ? 1 : 0);
         // (no stretch is behind the last block's, unless the lengths are written meanwhile by mistake)
-        const int64_t q1 = min(quotient(it.from + (static_cast<int64_t>(nt) << p.tile_shift) - half - 1, stretch),
+        const int64_t q1 = min(quotient(it.from + units_of((static_cast<int64_t>(nt) << p.tile_shift) - half, it.weight) - 1, stretch),
                                static_cast<int64_t>(gridDim.x) - 1);
         if (q0 < q1 && lane == 0)                // else one block writes it
             joins[blockIdx.x] = JoinItem{static_cast<int>(q1 - q0) + 1, line_slot(it, stretch, q0), it.s.q0, it.s.n, it.s.m, it.i, it.h, 0};
