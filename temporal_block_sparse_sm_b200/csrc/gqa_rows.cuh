@@ -17,6 +17,11 @@
 // maximum, sum and output, so warps meet only at the ring's barriers; their states are joined at
 // an item's end, while the ring already fills with the next item's keys.
 //
+// Measured (B200, bf16, D = 128, in a graph): 64 single tokens of 32 heads over 277,485 cached
+// tokens of 8 key heads, 1138 MB, 185 us (6140 GB/s, 0.94 of a plain copy); one token over 1,000
+// 12.5 us, of which walking to the first load and the join after the last part take 3 us each.  Q K^T
+// in two accumulators was slower.
+//
 // Values that no row sees (behind the last key, in a page's unused part) are zeroed in
 // shared memory before the product, since 0 * NaN is NaN.  Where some rows see a key that
 // others do not, and a value there is not finite, the product of those 16 keys is done

@@ -10,6 +10,10 @@
 // its token, so the angles cost one read per `head_lanes` threads and not one per head.
 // `head_lanes` threads of a token share its heads: many when there are few tokens (a
 // decoding step, where only latency counts), few when there are many.
+//
+// Measured (B200): 20,671 tokens of 24 query and 4 key heads of 128, 341 MB, 58 us in a graph
+// (5880 GB/s, 0.9 of a plain copy; the warps wait for their loads, 66% of the DRAM cycles are
+// used); 64 tokens of 32 and 8 heads 4 us, a launch and two dependent loads (table, then rows).
 #pragma once
 
 #include "serving_internal.cuh"

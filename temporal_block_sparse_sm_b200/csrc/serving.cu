@@ -154,7 +154,11 @@ struct Division {
     bool split;           // items may be cut
     size_t workspace;
 };
-// In keys, measured: the turn from one item to the next, and what partial outputs and their join cost.
+// In keys, measured: the turn from one item to the next, what partial outputs and their join cost,
+// and the shortest stretch.  Around them (26 shapes): a tile join cost of 640 made a prompt of 4,096 tokens
+// 70 -> 83 us and 1,000 tokens 24 -> 27, one of 320 worse still; a rows join cost of 160 16 tokens over 300 keys
+// 8.3 -> 12.5 us, one of 640 one token over 500 12.0 -> 12.7; a shortest tile stretch of 512 64 tokens
+// over 8,000 keys 23.7 -> 25.7 us (300 over 2,300: 28.0 -> 27.0).
 constexpr int kTileItemCost = 256, kTileJoinCost = 1280, kTileMinStretch = 256;
 constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 128;
 // Eighths of a key that a key costs an item whose second slot is empty, measured: 6 at d = 128 (a
@@ -162,12 +166,14 @@ constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 128;
 // with 4), all 8 at d = 64 (880 tokens over 14,000 keys of 24 heads: 141 us with 8 or 6, 160 with
 // 5; 11 chunks of up to 513 tokens: 164 us with 8, 170 with 6).
 constexpr int kTileHalfWeight128 = 6, kTileHalfWeight64 = 8;
-constexpr int kManyItems = 8;   // items per block from which whole items come out even
+constexpr int kManyItems = 8;   // items per block from which whole items come out even within an eighth: no workspace
 
 Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_new, int64_t max_keys) {
     const int64_t G = pl->Hq / pl->Hk;
     max_new = std::min(max_new, tokens);
     Division dv;
+    // Up to one item's rows for the rows kernel, measured on both: 16 rows over 64 x 4,336 keys 60 us here, 65
+    // in tiles; over 8 x 2,000 keys of 8 heads 24 and 33; 32 rows 104 and 65, 31 and 33.
     dv.tile = max_new * G > RowsCfg<128>::ROWS;
     int64_t least;        // items of a batch without padding
     int most;             // blocks that run at the same time
