@@ -18,8 +18,8 @@
 // an item's end, while the ring already fills with the next item's keys.
 //
 // Measured (B200, bf16, D = 128, in a graph): 64 single tokens of 32 heads over 277,485 cached
-// tokens of 8 key heads, 1138 MB, 185 us (6140 GB/s, 0.94 of a plain copy); one token over 1,000
-// 12.5 us, of which walking to the first load and the join after the last part take 3 us each.  Q K^T
+// tokens of 8 key heads, 1138 MB, 186 us (6110 GB/s, 0.93 of a plain copy); one token over 1,000
+// 12.1 us, of which walking to the first load and the join after the last part take 3 us each.  Q K^T
 // in two accumulators was slower.
 //
 // Values that no row sees (behind the last key, in a page's unused part) are zeroed in
@@ -126,9 +126,8 @@ struct KvTiles {
     }
 };
 
-// The join may be launched while the kernel that writes the parts still runs, and waits for it.
+// The join may be launched while the kernel that writes the parts still runs.
 __device__ __forceinline__ void join_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // What the warps of a block need to know of one item (shared memory).
 struct RowsWork {
@@ -175,6 +174,7 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         s_abort = 0u;
         ptx::fence_barrier_init();
     }
+    wait_for_earlier_kernels();
     const int64_t stretch = stretch_units<C::NTHREADS>(pb, gridDim.x, scan);
     __syncthreads();
     join_may_start();
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(const GqaParams 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.b.G;
     const int rows = slot_tokens ? 256 : RowsCfg<D>::ROWS;
     auto rows_at_once = [](int parts) { return parts < 8 ? kJoinWarps : parts < 64 ? kJoinWarps / 4 : 1; };
-    wait_for_parts();
+    wait_for_earlier_kernels();
     // units (rows_at_once rows of an item) up to and with each record
     const int parts_here = threadIdx.x < blocks ? p.joins[threadIdx.x].parts : 0;
     int units = parts_here > 0 ? rows / rows_at_once(parts_here) : 0;

@@ -217,13 +217,14 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     GqaBatch pb = p.a.b;             // what is fixed for this kernel, as constants
     pb.tile_shift = 7;
     static_assert(BN == 128);
-    const int64_t stretch = stretch_units<C::NTHREADS>(pb, gridDim.x, scan);
-    join_may_start();
     const WaitScope wctx{&s_abort, pb.status};
     if (warp == 2) {
         ptx::tmem_alloc(ptx::smem_u32(&s_tmem), C::TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    wait_for_earlier_kernels();
+    const int64_t stretch = stretch_units<C::NTHREADS>(pb, gridDim.x, scan);
+    join_may_start();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();

@@ -12,7 +12,7 @@
 // decoding step, where only latency counts), few when there are many.
 //
 // Measured (B200): 20,671 tokens of 24 query and 4 key heads of 128, 341 MB, 58 us in a graph
-// (5880 GB/s, 0.9 of a plain copy; the warps wait for their loads, 66% of the DRAM cycles are
+// (5850 GB/s, 0.9 of a plain copy; the warps wait for their loads, 66% of the DRAM cycles are
 // used); 64 tokens of 32 and 8 heads 4 us, a launch and two dependent loads (table, then rows).
 #pragma once
 
@@ -44,6 +44,7 @@ struct AppendToken {
 template <bool F16>
 __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const AppendParams p) {
     __shared__ AppendToken tok[kAppendThreads];
+    wait_for_earlier_kernels();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens_per_block;
     if (threadIdx.x < p.tokens_per_block) {
         AppendToken a;

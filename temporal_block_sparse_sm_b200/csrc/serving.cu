@@ -207,24 +207,31 @@ Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_
     return dv;
 }
 
-// The kernel that joins split items, launched so that it may begin before the one in front of
-// it has ended (it waits for that one's results itself).
-template <int D, bool F16>
-int launch_join(const lite_attn_gqa *pl, const GqaParams &p, const Division &dv, int slot_tokens, cudaStream_t s) {
-    if (!dv.split) return LITE_OK;
+// Launches a kernel so that it may begin before the one in front of it on the stream has ended (the
+// kernels wait for that one themselves, wait_for_earlier_kernels).
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), int64_t blocks, int threads, uint32_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(dv.tile ? 4 * pl->sms : pl->sms);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const int rc = cuda_err(cudaLaunchKernelEx(&cfg, gqa_join_kernel<D, F16>, p, slot_tokens, dv.blocks));
+    const int rc = cuda_err(cudaLaunchKernelEx(&cfg, kernel, args...));
     if (rc != LITE_OK) cudaGetLastError();
     else g_launches.fetch_add(1);
     return rc;
+}
+
+// Joins split items, if there may be any.
+template <int D, bool F16>
+int launch_join(const lite_attn_gqa *pl, const GqaParams &p, const Division &dv, int slot_tokens, cudaStream_t s) {
+    if (!dv.split) return LITE_OK;
+    return launch(gqa_join_kernel<D, F16>, dv.tile ? 4 * pl->sms : pl->sms, kJoinThreads, 0, s, p, slot_tokens, dv.blocks);
 }
 
 template <int D, bool F16>
@@ -234,9 +241,7 @@ int launch_rows(const lite_attn_gqa *pl, const CUtensorMap &tk, const CUtensorMa
     static std::atomic<bool> done[kMaxDevices];
     int rc = allow_smem(gqa_rows_kernel<D, F16>, done, pl->device, C::SMEM_BYTES);
     if (rc != LITE_OK) return rc;
-    gqa_rows_kernel<D, F16><<<dv.blocks, C::NTHREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
-    g_launches.fetch_add(1);
-    rc = cuda_err(cudaGetLastError());
+    rc = launch(gqa_rows_kernel<D, F16>, dv.blocks, C::NTHREADS, C::SMEM_BYTES, s, tk, tv, p);
     return rc == LITE_OK ? launch_join<D, F16>(pl, p, dv, 0, s) : rc;
 }
 
@@ -256,9 +261,7 @@ int launch_tile(const lite_attn_gqa *pl, const CUtensorMap &tq, const CUtensorMa
     }
     int rc = allow_smem(gqa_tile_kernel<D, F16>, done, pl->device, C::SMEM_BYTES);
     if (rc != LITE_OK) return rc;
-    gqa_tile_kernel<D, F16><<<dv.blocks, C::NTHREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, p);
-    g_launches.fetch_add(1);
-    rc = cuda_err(cudaGetLastError());
+    rc = launch(gqa_tile_kernel<D, F16>, dv.blocks, C::NTHREADS, C::SMEM_BYTES, s, tq, tk, tv, p);
     return rc == LITE_OK ? launch_join<D, F16>(pl, p.a, dv, p.slot_tokens, s) : rc;
 }
 
@@ -466,10 +469,7 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *a, vo
     p.tokens_per_block = slots / lanes;
     const int64_t blocks = (a->k.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (plan->dtype == LITE_DTYPE_FP16) rope_append_kernel<true><<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p);
-    else rope_append_kernel<false><<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p);
-    g_launches.fetch_add(1);
-    return cuda_err(cudaGetLastError());
+    return launch(plan->dtype == LITE_DTYPE_FP16 ? rope_append_kernel<true> : rope_append_kernel<false>, blocks, kAppendThreads, 0, s, p);
 }
 
 int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *a, void *stream) {

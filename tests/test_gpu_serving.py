@@ -741,3 +741,75 @@ def test_too_many_keys_are_refused():
 ])
 def test_items_of_one_slot_and_of_two(Hq, Hk, d, dtype, new, total, causal):
     _attend_case(Hq, Hk, d, dtype, 32, "bhnd", new, total, causal=causal, seed=len(new), pad=3)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("new", [1, 40])
+def test_calls_wait_for_whatever_is_in_front_of_them(new, captured):
+    """Inputs written right before each call by kernels, copies and another stream, outputs read right
+    after it, without a wait on the host: the same as with one between all of them."""
+    from temporal_block_sparse_sm_b200 import serving
+    g = _gen(71)
+    Hq, Hk, d, page, steps = 8, 2, 128, 16, 6
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    src = [[_randn(g, 2 * new, h, d, dtype=BF16) for h in (Hq, Hk, Hk)] for _ in range(steps)]
+    table = torch.randperm(2 * 140, device="cuda", generator=g).int().view(2, 140)
+    big = _randn(g, 4096, 4096, dtype=BF16)
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def run(sync):
+        kp, vp = (torch.zeros(2 * 140, Hk, page, d, dtype=BF16, device="cuda") for _ in range(2))
+        lens = torch.full((2,), 2000, dtype=torch.int32, device="cuda")
+        cu, outs = offsets([new, new]), [torch.zeros(2 * new, Hq, d, dtype=BF16, device="cuda") for _ in range(steps)]
+        q, k, v = (torch.zeros_like(x) for x in src[0])
+        o, y = torch.zeros_like(q), torch.empty_like(big)
+        cache = serving.PagedCache(plan, kp, vp)
+
+        def step():
+            for i in range(steps):
+                torch.mul(big, 2, out=y)              # keeps the GPU busy, so that what comes next queues up
+                ev = torch.cuda.Event()
+                ev.record()
+                side.wait_event(ev)
+                with torch.cuda.stream(side):
+                    torch.add(y, 1, out=y)
+                    torch.add(src[i][2], 0, out=v)
+                    done = torch.cuda.Event()
+                    done.record()
+                lens.add_(new)
+                q.copy_(src[i][0])
+                k.copy_(src[i][1])
+                torch.cuda.current_stream().wait_event(done)
+                if sync:
+                    torch.cuda.synchronize()
+                cache.append(k, v, lens, cu, table)
+                if sync:
+                    torch.cuda.synchronize()
+                cache.attend(q, o, lens, cu, table, max_new=new)
+                if sync:
+                    torch.cuda.synchronize()
+                outs[i].copy_(o)
+                o.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(main):
+            if captured and not sync:
+                step()                                # warm-up
+                torch.cuda.synchronize()
+                for t in (kp, vp):
+                    t.zero_()
+                lens.fill_(2000)
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=main):
+                    step()
+                graph.replay()
+            else:
+                step()
+        torch.cuda.synchronize()
+        plan.check()
+        return outs, kp, vp
+
+    want, got = run(True), run(False)
+    for a, b in zip(want[0], got[0]):
+        assert torch.equal(a, b)
+    assert torch.equal(want[1], got[1]) and torch.equal(want[2], got[2])
