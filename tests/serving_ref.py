@@ -8,14 +8,15 @@ row does not see are left out of its sums altogether.
 The bound, per element.  Let u = eps / 2 of the 16-bit type (a rounding is off by at most
 half a step), A = sum_j w_j |v_j| and o the exact output.
 * The weights enter the product rounded to 16 bits, w_j (1 + e_j) with |e_j| <= u, and are
-  normalised by a sum of the rounded weights: the result moves by at most
-  |sum w_j e_j (v_j - o)| / (1 - u) <= u (A + |o|) / (1 - u) <= 2 u A / (1 - u).
+  normalised by the sum of the weights before or after that rounding: the result moves by at most
+  u A, or |sum w_j e_j (v_j - o)| / (1 - u) <= u (A + |o|) / (1 - u) <= 2 u A / (1 - u).
 * A logit is a sum of d products in 32 bits: off by at most d 2^-23 scale sum |q||k| =: s
   (twice the half-step, for accumulations that do not round to nearest), so a weight is off by
   a factor within exp(+-2 s) after normalisation: 2 (exp(2 s) - 1) A.
-* The exponential is off by at most x: 2^-13 for bf16 (a polynomial of maximum relative error
-  7.5e-5 on some of the weights), 2^-17 for fp16; and its argument, held in 32 bits, by
-  2^-23 of its own size (the size of the logits, at most 2 * scale sum |q||k|), so 2 (x + 2^-22 L) A.
+* The exponential is off by at most x = 2^-18 (the hardware's 2^x is off by 2^-22: in the weight, and
+  in each rescaling of the sums that hold it, of which 15 are allowed for); and its argument, held
+  in 32 bits, by 2^-23 of its own size (the size of the logits, at most 2 * scale sum |q||k|), so
+  2 (x + 2^-22 L) A.
 * Sums of m terms in 32 bits, in an order that is not fixed here: 2^-24 m^(1/2) would be typical,
   2^-24 m is sure: 2 m 2^-24 A.
 * The output is rounded once: u |o| (and half the smallest step of the type).
@@ -34,7 +35,7 @@ def seq_reference(q, k, v, causal, scale):
     G = Hq // Hk
     dt = q.dtype
     u = torch.finfo(dt).eps / 2
-    x = 2.0 ** -17 if dt == torch.float16 else 2.0 ** -13
+    x = 2.0 ** -18
     o = torch.zeros(n, Hq, d, dtype=torch.float64, device=q.device)
     tol = torch.full_like(o, torch.finfo(dt).smallest_normal * torch.finfo(dt).eps)
     sees = torch.arange(n, device=q.device) + (m - n + 1) if causal else torch.full((n,), m, device=q.device)
