@@ -11,10 +11,9 @@
 // item is a single slot, and the second one idle.)  Each slot owns 128
 // TMEM columns of S and D of O; P is written over S and read by the MMA from TMEM.
 //
-// Blocks are persistent, one per SM: segment x of the batch goes to block x mod grid, back
-// and forth (the order has the longest first, so the blocks' sums come out alike).  The next
-// item's queries, keys and first product overlap the current one's last softmax and its
-// epilogue.
+// Blocks are persistent, one per SM, and take whole items or stretches of the batch
+// (serving_internal.cuh).  The next item's queries, keys and first product overlap the current
+// one's last softmax and its epilogue.
 //
 // Warps: 0 loads (TMA: Q of a slot when its last product with K is done, 128-key tiles of K
 // and V into rings), 1 and 2 issue the MMAs of slot 0 and 1, 3 walks the work items and cleans

@@ -11,7 +11,9 @@
 // the batch for the block's items (BlockWalk).
 //
 // Division among the blocks.  A batch of many items (block of query rows, key head) is dealt
-// out whole, in order of length within a sequence, back and forth over the blocks.  With few
+// out whole, in order of length within a sequence: of one sequence back and forth over the blocks,
+// of several by a counter, to whichever block asks next (an item's result does not depend on its
+// block; back and forth, the longest block of a ragged batch had a quarter more than the mean).  With few
 // items the batch is laid out on a line instead, an item taking as many units as its last row
 // sees keys (half_weight eighths of that where it fills only the first of the tile kernel's two
 // slots), and item_cost for its start and end; each block takes an equal stretch of the line,
@@ -48,6 +50,7 @@ struct GqaBatch {
     int unit_tokens;       // query tokens of a work item; 0: kFewRows rows (token, head of the group)
     int tile_shift;        // log2 of the keys of a tile
     int may_split;         // items may be cut
+    int *next_item;        // zero before the kernel: items handed out, but for each block's first; null: back and forth
     // in keys: what an item costs beside its keys, what partial outputs and their join cost, and
     // the shortest stretch (more than a tile, so that no stretch inside an item is without one)
     int item_cost, join_cost, min_stretch;
@@ -347,7 +350,11 @@ struct BlockWalk {
         int64_t first;
         if (stretch == 0) {         // whole items, back and forth over the blocks
             const int grid = static_cast<int>(gridDim.x), blk = static_cast<int>(blockIdx.x);
-            const int64_t item = x * grid + ((x & 1) ? grid - 1 - blk : blk);
+            int64_t item = x * grid + ((x & 1) ? grid - 1 - blk : blk);
+            if (p.next_item && x > 0) {
+                const int taken = lane == 0 ? atomicAdd(p.next_item, 1) : 0;
+                item = static_cast<int64_t>(grid) + __shfl_sync(0xFFFFFFFFu, taken, 0);
+            }
             ++x;
             if (!cur.find(p, false, lane, item, b, s, nb, first)) return false;
             const int y = static_cast<int>(item - first);

@@ -813,3 +813,33 @@ def test_calls_wait_for_whatever_is_in_front_of_them(new, captured):
     for a, b in zip(want[0], got[0]):
         assert torch.equal(a, b)
     assert torch.equal(want[1], got[1]) and torch.equal(want[2], got[2])
+
+
+@pytest.mark.parametrize("Hq,Hk,d,dtype,B,top", [(16, 8, 64, BF16, 60, 300), (12, 12, 128, FP16, 33, 1), (8, 8, 64, BF16, 400, 2)])
+def test_items_handed_out_by_a_counter(Hq, Hk, d, dtype, B, top):
+    """More items than blocks in a ragged batch, eager and in a graph that is replayed: the same, and right."""
+    import random
+    from temporal_block_sparse_sm_b200 import serving
+    r, g = random.Random(B), _gen(B)
+    new = [r.randint(1, top) for _ in range(B)]
+    nk = [n + r.randint(0, 300) for n in new]
+    q = _randn(g, sum(new), Hq, d, dtype=dtype)
+    k, v = (_randn(g, sum(nk), Hk, d, dtype=dtype) for _ in range(2))
+    plan, cu_q, cu_k, o = serving.GroupedPlan(Hq, Hk, d, dtype=dtype), offsets(new), offsets(nk), torch.zeros_like(q)
+    plan.prompt(q, k, v, o, cu_q, cu_k)
+    plan.check()
+    eager = o.clone()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        plan.prompt(q, k, v, o, cu_q, cu_k)
+        plan.prompt(q, k, v, o, cu_q, cu_k)
+    for _ in range(3):
+        o.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager)
+    for b in range(0, B, max(1, B // 20)):
+        i, j = sum(new[:b]), sum(nk[:b])
+        want, tol = seq_reference(q[i:i + new[b]], k[j:j + nk[b]], v[j:j + nk[b]], True, 1 / math.sqrt(d))
+        assert_close(eager[i:i + new[b]], want, tol, f"sequence {b}")
