@@ -305,6 +305,8 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                         bad |= nonfinite16<F16>(v.x) | nonfinite16<F16>(v.y) | nonfinite16<F16>(v.z) | nonfinite16<F16>(v.w);
                     }
                 }
+                // the stage's next writer is TMA, by another proxy than these stores: ordered by this fence and the arrival
+                ptx::fence_proxy_async();
                 scalar = __any_sync(0xFFFFFFFFu, bad != 0u);
                 __syncwarp();
             }

@@ -329,7 +329,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                 }
                             }
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMA reads what was written here
+                    ptx::fence_proxy_async();   // the MMA reads what was written here
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(v_ok(st));
                 }

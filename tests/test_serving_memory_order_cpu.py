@@ -1,0 +1,28 @@
+"""Orders between memory accesses that the serving kernels rely on and that no run can show to be
+missing: read from the kernels' sources."""
+from __future__ import annotations
+
+import os
+import re
+
+from temporal_block_sparse_sm_b200 import build as lib_build
+
+KERNELS = ("serving_internal.cuh", "rope_append.cuh", "gqa_rows.cuh", "gqa_tile.cuh")
+
+
+def source(name):
+    """A source file without its comments."""
+    with open(os.path.join(lib_build.CSRC, name)) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", text, flags=re.S))
+
+
+def test_values_zeroed_in_the_ring_are_ordered_before_the_next_copy():
+    """A ring stage is written with ordinary stores (hidden values zeroed) and next by TMA: a proxy fence
+    lies between the stores and the arrival that frees the stage."""
+    for name, start, end in (("gqa_rows.cuh", "*at = make_uint4(0u, 0u, 0u, 0u);", "mbar_arrive(empty(st))"),
+                             ("gqa_tile.cuh", "= make_uint4(0u, 0u, 0u, 0u);", "mbar_arrive(v_ok(st))")):
+        text = source(name)
+        assert text.count(start) == 1 and text.count(end) == 1
+        between = text[text.index(start):text.index(end)]
+        assert "fence_proxy_async()" in between or "fence.proxy.async.shared::cta" in between, name
