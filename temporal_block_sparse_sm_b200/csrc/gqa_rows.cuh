@@ -108,7 +108,7 @@ struct KvTiles {
     __device__ __forceinline__ int page_of(int t, int lane) const {
         if (lane >= boxes(t)) return -1;
         if (p.mode == kKvPacked) return 0;
-        const int pg = __ldg(p.table + static_cast<int64_t>(b) * p.table_w + ((t * BN + lane * box) >> p.page_shift));
+        const int pg = load_int(p.table + static_cast<int64_t>(b) * p.table_w + ((t * BN + lane * box) >> p.page_shift));
         if (pg >= 0 && pg < p.pages) return pg;
         atomicExch(p.status, kStatusCheck);
         return static_cast<int>(p.pages);   // outside the tensor map: reads as zeros
@@ -254,8 +254,8 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                                                                  (static_cast<int64_t>(w.h) * G + g) * p.q_sh);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            qf[kk][r] = ok ? __ldg(src + kk * 8 + tig) : 0u;
-            qf[kk][2 + r] = ok ? __ldg(src + kk * 8 + 4 + tig) : 0u;
+            qf[kk][r] = ok ? src[kk * 8 + tig] : 0u;
+            qf[kk][2 + r] = ok ? src[kk * 8 + 4 + tig] : 0u;
         }
     }
     float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};

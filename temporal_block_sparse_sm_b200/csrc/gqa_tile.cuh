@@ -655,7 +655,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     int64_t from = (tw.k0 + key) * p.v_token;
                     if (pb.mode != kKvPacked) {
                         // checked here too: it is the second look, and the table may be written meanwhile by mistake
-                        const int pg = __ldg(pb.table + static_cast<int64_t>(tw.b) * pb.table_w + (key >> pb.page_shift));
+                        const int pg = load_int(pb.table + static_cast<int64_t>(tw.b) * pb.table_w + (key >> pb.page_shift));
                         if (pg < 0 || pg >= pb.pages) {
                             atomicExch(pb.status, kStatusCheck);
                             continue;
@@ -667,7 +667,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     for (int i = 0; i < 16; ++i) {
                         float a, b;
                         uint32_t v;
-                        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(src + i));   // one at a time: few registers
+                        asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(src + i));   // one at a time: few registers
                         const uint32_t bad = nonfinite16<F16>(v);
                         unpack16<F16>(v, a, b);
                         if (bad & 0x8000u) o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) + a);

@@ -52,20 +52,20 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const Appen
         a.pos = -1;
         a.pad = 0;
         const int64_t t = t0 + threadIdx.x;
-        const int first = __ldg(p.b.cu_q), last = __ldg(p.b.cu_q + p.b.B);
+        const int first = load_int(p.b.cu_q), last = load_int(p.b.cu_q + p.b.B);
         if (t < p.b.Tq && t >= first && t < last) {
             int lo = 0, hi = p.b.B;   // cu_q[lo] <= t < cu_q[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (__ldg(p.b.cu_q + mid) <= t) lo = mid;
+                if (load_int(p.b.cu_q + mid) <= t) lo = mid;
                 else hi = mid;
             }
             const SeqInfo s = seq_info(p.b, lo);
             const int64_t slot = static_cast<int64_t>(s.m) - s.n + (t - s.q0);
             int pg = -1;
             if (s.n > 0 && t < s.q0 + s.n && slot >= 0)
-                pg = __ldg(p.b.table + static_cast<int64_t>(lo) * p.b.table_w + (slot >> p.b.page_shift));
-            const int64_t pos = p.positions ? __ldg(p.positions + t) : slot;
+                pg = load_int(p.b.table + static_cast<int64_t>(lo) * p.b.table_w + (slot >> p.b.page_shift));
+            const int64_t pos = p.positions ? load_int(p.positions + t) : slot;
             if (pg < 0 || pg >= p.b.pages || (p.cos && (pos < 0 || pos >= p.n_pos))) {
                 atomicExch(p.b.status, kStatusCheck);   // nothing of this token is written
             } else {
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const Appen
     if (turn) {
         const float4 *pc = reinterpret_cast<const float4 *>(p.cos + static_cast<int64_t>(a.pos) * (p.rot / 2) + 8 * chunk);
         const float4 *ps = reinterpret_cast<const float4 *>(p.sin + static_cast<int64_t>(a.pos) * (p.rot / 2) + 8 * chunk);
-        const float4 c0 = __ldg(pc), c1 = __ldg(pc + 1), s0 = __ldg(ps), s1 = __ldg(ps + 1);
+        const float4 c0 = pc[0], c1 = pc[1], s0 = ps[0], s1 = ps[1];
         c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
         s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
     }

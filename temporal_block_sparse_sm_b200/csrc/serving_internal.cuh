@@ -57,6 +57,15 @@ struct GqaBatch {
     int half_weight;       // eighths of a key that a key costs an item of no more than half unit_tokens
 };
 
+// A length, offset, page or position.  The kernel in front may still write it when this one starts, so it is
+// loaded coherently (the non-coherent path is for data that does not change during the kernel's life) and in
+// program order with the wait for that kernel; and once, so that what was checked is what is used.
+__device__ __forceinline__ int load_int(const int32_t *p) {
+    int x;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(p));
+    return x;
+}
+
 struct SeqInfo {
     int q0, n, m;
     int64_t k0;
@@ -66,18 +75,18 @@ struct SeqInfo {
 // that names rows or keys outside them has no work, and the plan's status says so.
 __device__ __forceinline__ SeqInfo seq_info(const GqaBatch &p, int b) {
     SeqInfo s;
-    s.q0 = __ldg(p.cu_q + b);
-    const int q1 = __ldg(p.cu_q + b + 1);
+    s.q0 = load_int(p.cu_q + b);
+    const int q1 = load_int(p.cu_q + b + 1);
     s.n = q1 - s.q0;
     s.k0 = 0;
     bool bad = s.q0 < 0 || q1 < s.q0 || q1 > p.Tq;
     if (p.mode == kKvPacked) {
-        const int k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+        const int k0 = load_int(p.cu_k + b), k1 = load_int(p.cu_k + b + 1);
         s.k0 = k0;
         s.m = k1 - k0;
         bad = bad || k0 < 0 || k1 < k0 || k1 > p.Tk;
     } else {
-        s.m = __ldg(p.lens + b);
+        s.m = load_int(p.lens + b);
         bad = bad || s.m < 0 || s.m > p.max_keys;
     }
     if (bad) {

@@ -26,3 +26,13 @@ def test_values_zeroed_in_the_ring_are_ordered_before_the_next_copy():
         assert text.count(start) == 1 and text.count(end) == 1
         between = text[text.index(start):text.index(end)]
         assert "fence_proxy_async()" in between or "fence.proxy.async.shared::cta" in between, name
+
+
+def test_loads_of_what_earlier_kernels_write_are_coherent():
+    """The kernels may start while the one in front of them still writes their inputs.  The non-coherent
+    path (ld.global.nc, __ldg, __restrict__ const pointers) is for data that nobody writes during a
+    kernel's whole life, and its loads may be moved in front of the wait for the earlier kernel."""
+    for name in KERNELS:
+        text = source(name)
+        for form in ("__ldg", "ld.global.nc", "__restrict__", "__ldcv", "__ldlu"):
+            assert form not in text, f"{name}: {form}"
