@@ -217,17 +217,19 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     pb.tile_shift = 7;
     static_assert(BN == 128);
     const WaitScope wctx{&s_abort, pb.status};
+    wait_for_earlier_kernels();
+    // Only now: a block that held the SM's Tensor Memory while it waits would keep blocks of the kernel in
+    // front from allocating theirs, and neither would end.
     if (warp == 2) {
         ptx::tmem_alloc(ptx::smem_u32(&s_tmem), C::TMEM_COLS);
         ptx::tmem_relinquish();
     }
-    wait_for_earlier_kernels();
     const int64_t stretch = stretch_units<C::NTHREADS>(pb, gridDim.x, scan);
-    join_may_start();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t *>(&s_tmem));
+    join_may_start();    // behind the allocation too, for the same reason
     auto wait_all = [&](uint32_t bar, uint32_t par) { return wait_phase_warp(bar, par, wctx); };
 
     if (warp < 4) {

@@ -36,3 +36,13 @@ def test_loads_of_what_earlier_kernels_write_are_coherent():
         text = source(name)
         for form in ("__ldg", "ld.global.nc", "__restrict__", "__ldcv", "__ldlu"):
             assert form not in text, f"{name}: {form}"
+
+
+def test_tensor_memory_is_taken_after_the_wait_for_earlier_kernels():
+    """A block that started early and holds all of an SM's Tensor Memory while it waits for the kernel in
+    front would keep that kernel's blocks there from allocating theirs: neither would ever end."""
+    text = source("gqa_tile.cuh")
+    assert text.count("wait_for_earlier_kernels();") == 1 and text.count("ptx::tmem_alloc(") == 1
+    assert text.index("wait_for_earlier_kernels();") < text.index("ptx::tmem_alloc(") < text.index("join_may_start();")
+    rows = source("gqa_rows.cuh")
+    assert "tmem_alloc" not in rows
