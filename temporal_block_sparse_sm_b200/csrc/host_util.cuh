@@ -28,10 +28,44 @@ struct NvtxRange {
     NvtxRange &operator=(const NvtxRange &) = delete;
 };
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using PtrAttrsFn = CUresult (*)(unsigned int, CUpointer_attribute *, void **, CUdeviceptr);
+using CtxGetFn = CUresult (*)(CUcontext *);
+
+struct DriverFns {
+    EncodeTiledFn encode = nullptr;
+    PtrAttrsFn ptr_attrs = nullptr;
+    CtxGetFn ctx_get = nullptr;
+    bool ok = false;
+};
+
+inline const DriverFns &driver() {
+    static DriverFns fns;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        cudaDriverEntryPointQueryResult q1, q2, q3;
+        void *p1 = nullptr, *p2 = nullptr, *p3 = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p1, cudaEnableDefault, &q1) == cudaSuccess &&
+            q1 == cudaDriverEntryPointSuccess)
+            fns.encode = reinterpret_cast<EncodeTiledFn>(p1);
+        if (cudaGetDriverEntryPoint("cuPointerGetAttributes", &p2, cudaEnableDefault, &q2) == cudaSuccess &&
+            q2 == cudaDriverEntryPointSuccess)
+            fns.ptr_attrs = reinterpret_cast<PtrAttrsFn>(p2);
+        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p3, cudaEnableDefault, &q3) == cudaSuccess &&
+            q3 == cudaDriverEntryPointSuccess)
+            fns.ctx_get = reinterpret_cast<CtxGetFn>(p3);
+        fns.ok = fns.encode && fns.ptr_attrs && fns.ctx_get;
+    });
+    return fns;
+}
+
 // Makes a plan's device current for the duration of a call and gives the caller
 // back its own current device on exit, so a plan works whichever device the
 // calling thread has selected (kernels, copies, events and synchronisation all
-// go to the device that owns the plan's memory).
+// go to the device that owns the plan's memory).  A thread that has not used CUDA
+// yet has no context, which the driver calls here need: it gets the device's.
 struct DeviceScope {
     int prev = -1;
     bool ok = false;
@@ -41,7 +75,9 @@ struct DeviceScope {
             prev = -1;
             return;
         }
-        ok = prev == device || cudaSetDevice(device) == cudaSuccess;
+        CUcontext ctx = nullptr;
+        const bool bound = prev == device && driver().ok && driver().ctx_get(&ctx) == CUDA_SUCCESS && ctx;
+        ok = bound || cudaSetDevice(device) == cudaSuccess;
     }
     ~DeviceScope() {
         int cur = -1;
@@ -61,34 +97,6 @@ constexpr int kMaxDevices = 64;
 inline bool fault(const char *what) {
     const char *e = std::getenv("LITE_ATTN_FAULT");
     return e && std::strcmp(e, what) == 0;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-using PtrAttrsFn = CUresult (*)(unsigned int, CUpointer_attribute *, void **, CUdeviceptr);
-
-struct DriverFns {
-    EncodeTiledFn encode = nullptr;
-    PtrAttrsFn ptr_attrs = nullptr;
-    bool ok = false;
-};
-
-inline const DriverFns &driver() {
-    static DriverFns fns;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        cudaDriverEntryPointQueryResult q1, q2;
-        void *p1 = nullptr, *p2 = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p1, cudaEnableDefault, &q1) == cudaSuccess &&
-            q1 == cudaDriverEntryPointSuccess)
-            fns.encode = reinterpret_cast<EncodeTiledFn>(p1);
-        if (cudaGetDriverEntryPoint("cuPointerGetAttributes", &p2, cudaEnableDefault, &q2) == cudaSuccess &&
-            q2 == cudaDriverEntryPointSuccess)
-            fns.ptr_attrs = reinterpret_cast<PtrAttrsFn>(p2);
-        fns.ok = fns.encode && fns.ptr_attrs;
-    });
-    return fns;
 }
 
 inline int cuda_err(cudaError_t e) { return e == cudaSuccess ? LITE_OK : LITE_ERR_CUDA; }
