@@ -103,20 +103,26 @@ inline int cuda_err(cudaError_t e) { return e == cudaSuccess ? LITE_OK : LITE_ER
 
 // Checks that [ptr, ptr + bytes) is device memory of `device` inside one allocation,
 // and that ptr is aligned to `align` bytes (a power of two).
-// One driver call (a serving step asks a dozen times).
+// One driver call (a serving step asks a dozen times); a second where the allocation may be a
+// reserved range of addresses of which only a part is mapped (virtual memory management, pools):
+// there the last byte must be mapped too.
 inline bool device_range_ok(const void *ptr, size_t bytes, int device, uintptr_t align = 16) {
-    if (!ptr || (reinterpret_cast<uintptr_t>(ptr) & (align - 1u))) return false;
+    if (!ptr || (reinterpret_cast<uintptr_t>(ptr) & (align - 1u)) || !driver().ok) return false;
     unsigned int type = 0, managed = 0;
     int ordinal = -1;
-    CUdeviceptr start = 0;
-    size_t size = 0;
-    CUpointer_attribute which[5] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
-                                    CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE};
-    void *out[5] = {&type, &managed, &ordinal, &start, &size};
-    if (driver().ptr_attrs(5, which, out, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS) return false;
+    CUdeviceptr start = 0, mapped_at = 0;
+    size_t size = 0, mapped = 0;
+    CUpointer_attribute which[7] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL,
+                                    CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, CU_POINTER_ATTRIBUTE_RANGE_SIZE,
+                                    CU_POINTER_ATTRIBUTE_MAPPING_BASE_ADDR, CU_POINTER_ATTRIBUTE_MAPPING_SIZE};
+    void *out[7] = {&type, &managed, &ordinal, &start, &size, &mapped_at, &mapped};
+    if (driver().ptr_attrs(7, which, out, reinterpret_cast<CUdeviceptr>(ptr)) != CUDA_SUCCESS) return false;
     if (!managed && (type != CU_MEMORYTYPE_DEVICE || ordinal != device)) return false;
-    const uintptr_t b = static_cast<uintptr_t>(start), x = reinterpret_cast<uintptr_t>(ptr);
-    return x >= b && x - b + bytes <= size;
+    const uintptr_t b = static_cast<uintptr_t>(start), m = static_cast<uintptr_t>(mapped_at), x = reinterpret_cast<uintptr_t>(ptr);
+    if (x < b || bytes > size || x - b > size - bytes) return false;
+    if (managed || bytes == 0 || (x >= m && x - m <= mapped && bytes <= mapped - (x - m))) return true;
+    return driver().ptr_attrs(3, which, out, static_cast<CUdeviceptr>(x + bytes - 1)) == CUDA_SUCCESS &&
+           type == CU_MEMORYTYPE_DEVICE && ordinal == device;
 }
 
 }  // namespace lite
