@@ -136,6 +136,33 @@ struct RowsWork {
     int whole, slot, valid;
 };
 
+// Weights for the product, each as two 16-bit numbers: the weight rounded towards zero, and what that left
+// over.  The kernel is bound by memory, so the second product costs next to nothing (0 to 1 %), and the
+// weights' rounding, as large as the output's own, is gone.  The second number of a weight is positive where
+// the first is, so that an infinite value stays infinite (0 * infinity is NaN).  What is added for that, of a
+// weight p:
+// bf16: at most 2^-17 p, as much as the second number's own rounding (or 2^-133, the type's least, where p is
+//   below 2^-116).
+// fp16: the type ends at 2^-24 and 65,504, so weights are taken relative to the largest of the 16 keys of a
+//   step, at 2^15: at most 2^-39 of that one, and as much for the rounding of small weights.  The largest weights of
+//   all steps are no more than the row's sum, so both stay below 16 * 2^-39 of it, however many keys there are;
+//   relative to the row's largest weight they would grow with the keys (a row of 9,000 keys at 2^-40 of its largest
+//   under values of 60,000 came out as 0.0014 instead of 0.0005).
+constexpr float kGroupBias = 15.0f;
+
+template <bool F16>
+__device__ __forceinline__ float second_number(float p, float first) {
+    if constexpr (F16) return first > 0.0f ? fmaxf(p - first, 0x1p-24f) : p;
+    else return p > 0.0f ? fmaxf(p - first, fmaxf(p * 0x1p-17f, 0x1p-133f)) : 0.0f;
+}
+template <bool F16>
+__device__ __forceinline__ void split16(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+    hi = pack16_down<F16>(p0, p1);
+    float h0, h1;
+    unpack16<F16>(hi, h0, h1);
+    lo = pack16<F16>(second_number<F16>(p0, h0), second_number<F16>(p1, h1));
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(RowsCfg<D>::NTHREADS, 2)
 gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
@@ -310,13 +337,14 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 scalar = __any_sync(0xFFFFFFFFu, bad != 0u);
                 __syncwarp();
             }
-            float alpha[2];
+            float alpha[2], top[2];       // the largest logit of these keys
             bool moved = false;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+                top[r] = mx;
                 alpha[r] = 1.0f;
                 if (mx - m_ref[r] > resc) {             // also the row's first finite maximum
                     alpha[r] = ptx::ex2((m_ref[r] - mx) * cl2);
@@ -332,28 +360,27 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     acc[n][2] *= alpha[1], acc[n][3] *= alpha[1];
                 }
             }
-            // Weights for the product, each as two 16-bit numbers, the weight rounded towards zero and
-            // what that left over: the kernel is bound by memory, so the second product costs next to
-            // nothing (0 to 1 %), and the weights' rounding, as large as the output's own, is gone.  Both
-            // are positive for a positive weight, so that an infinite value stays one.
-            float neg[2];
+            // weights, in the place of the logits: of bf16 relative to the running reference; of fp16, whose range
+            // is short, relative to the largest of these 16 keys (f brings the product into the frame of the sums)
+            float f[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) neg[r] = (m_ref[r] == -INFINITY ? 0.0f : -m_ref[r] * cl2) + weight_bias<F16>();
-            uint32_t pf[4], pl[4];
+            for (int r = 0; r < 2; ++r) {
+                const float ref = F16 ? top[r] : m_ref[r];
+                const float neg = ref == -INFINITY ? 0.0f : F16 ? fmaf(-ref, cl2, kGroupBias) : -ref * cl2;
+                f[r] = !F16 ? 1.0f : ref == -INFINITY ? 0.0f : ptx::ex2(fmaf(ref - m_ref[r], cl2, -kGroupBias));
+                float sum = 0.0f;
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
+                for (int nb = 0; nb < 2; ++nb) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p0 = ptx::ex2(fmaf(sc[nb][2 * r], cl2, neg[r])), p1 = ptx::ex2(fmaf(sc[nb][2 * r + 1], cl2, neg[r]));
-                    const int x = nb * 2 + r;
-                    pf[x] = pack16_down<F16>(p0, p1);
-                    float h0, h1;
-                    unpack16<F16>(pf[x], h0, h1);
-                    constexpr float tiny = F16 ? 0x1p-24f : 0x1p-100f;
-                    pl[x] = pack16<F16>(p0 > 0.0f ? fmaxf(p0 - h0, tiny) : 0.0f, p1 > 0.0f ? fmaxf(p1 - h1, tiny) : 0.0f);
-                    l[r] += p0 + p1;
+                    for (int i = 2 * r; i < 2 * r + 2; ++i) sc[nb][i] = ptx::ex2(fmaf(sc[nb][i], cl2, neg));
+                    sum += sc[nb][2 * r] + sc[nb][2 * r + 1];
                 }
+                l[r] = fmaf(sum, f[r], l[r]);
+            }
             if (!scalar) {
+                uint32_t pf[4], pl[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) split16<F16>(sc[x >> 1][2 * (x & 1)], sc[x >> 1][2 * (x & 1) + 1], pf[x], pl[x]);
                 // matrices of V: (keys 0-7, d n..n+7), (keys 8-15, same d), then the next 8 d
                 const int key = warp * 16 + (mi & 1) * 8 + mr;
                 const uint32_t rowa = vt + key * 128u;
@@ -362,10 +389,23 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const uint32_t c16 = (n & 3) * 2 + (mi >> 1);
                     uint32_t b0, b1, b2, b3;
                     ptx::ldsm4t(rowa + (n >> 2) * C::CHUNK_BYTES + ((c16 ^ (key & 7)) << 4), b0, b1, b2, b3);
-                    ptx::mma16816<F16>(acc[2 * n], pf, b0, b1);
-                    ptx::mma16816<F16>(acc[2 * n + 1], pf, b2, b3);
-                    ptx::mma16816<F16>(acc[2 * n], pl, b0, b1);
-                    ptx::mma16816<F16>(acc[2 * n + 1], pl, b2, b3);
+                    if constexpr (F16) {
+                        float t0[4] = {}, t1[4] = {};
+                        ptx::mma16816<F16>(t0, pf, b0, b1);
+                        ptx::mma16816<F16>(t1, pf, b2, b3);
+                        ptx::mma16816<F16>(t0, pl, b0, b1);
+                        ptx::mma16816<F16>(t1, pl, b2, b3);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            acc[2 * n][j] = fmaf(t0[j], f[j >> 1], acc[2 * n][j]);
+                            acc[2 * n + 1][j] = fmaf(t1[j], f[j >> 1], acc[2 * n + 1][j]);
+                        }
+                    } else {
+                        ptx::mma16816<F16>(acc[2 * n], pf, b0, b1);
+                        ptx::mma16816<F16>(acc[2 * n + 1], pf, b2, b3);
+                        ptx::mma16816<F16>(acc[2 * n], pl, b0, b1);
+                        ptx::mma16816<F16>(acc[2 * n + 1], pl, b2, b3);
+                    }
                 }
             } else {
 #pragma unroll 1
@@ -374,10 +414,8 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     float wt[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        float a, b, c, d;
-                        unpack16<F16>(__shfl_sync(0xFFFFFFFFu, key < 8 ? pf[r] : pf[2 + r], from), a, b);
-                        unpack16<F16>(__shfl_sync(0xFFFFFFFFu, key < 8 ? pl[r] : pl[2 + r], from), c, d);
-                        wt[r] = (key & 1) ? b + d : a + c;
+                        const float a = key < 8 ? sc[0][2 * r] : sc[1][2 * r], b = key < 8 ? sc[0][2 * r + 1] : sc[1][2 * r + 1];
+                        wt[r] = f[r] * __shfl_sync(0xFFFFFFFFu, (key & 1) ? b : a, from);
                     }
                     const bool see0 = kb + key < lim[0], see1 = kb + key < lim[1];
 #pragma unroll

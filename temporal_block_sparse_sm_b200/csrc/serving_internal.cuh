@@ -433,9 +433,9 @@ __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {
 }
 
 // ---------------------------------------------------------------- 16-bit types
-// Weights are 2^(x + bias): fp16 ones are scaled by 2^7, so that they lose no precision to
-// subnormals until they are 2^-21 of the row's largest (which stays below 2^15).  The row's
-// sum carries the same factor.
+// The tile kernel's weights are 2^(x + bias): fp16 ones are scaled by 2^7, so that they lose no
+// precision to subnormals until they are 2^-21 of the row's largest (which stays below 2^15).  The
+// row's sum carries the same factor.
 template <bool F16>
 __device__ __forceinline__ constexpr float weight_bias() { return F16 ? 7.0f : 0.0f; }
 

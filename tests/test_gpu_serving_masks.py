@@ -56,3 +56,42 @@ def test_stages_with_hidden_values_are_used_again(dtype, d, new):
     o, refs = _attend(q, ks, vs, [new] * len(lens))
     for b, (rows, want, tol) in enumerate(refs):
         assert_close(o[rows], want, tol, f"sequence {b}")
+
+
+def _one_key_and_many_far_ones(dtype, d, new, m, gap, far):
+    """q and keys such that key 0 has the logit `gap` (in powers of two of the weight) above all others,
+    which are equal; the values of key 0 are 0, the others' +-far by column."""
+    q = torch.zeros(new, 2, d, device="cuda")
+    k, v = torch.zeros(m, 1, d, device="cuda"), torch.zeros(m, 1, d, device="cuda")
+    q[..., 0] = 1.0
+    k[0, 0, 0] = gap
+    v[1:] = far * torch.where(torch.arange(d, device="cuda") % 2 == 0, 1.0, -1.0)
+    return q.to(dtype), k.to(dtype), v.to(dtype), math.log(2.0)
+
+
+@pytest.mark.parametrize("dtype,far", [(FP16, 6e4), (BF16, 1e4)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gap,m", [(100, 1000), (40, 9000), (12, 1000)])
+def test_weights_far_below_the_largest_count_as_what_they_are(dtype, far, d, gap, m):
+    """Keys 2^-gap below the largest weight, whose key has no value: nothing is added to them, and what
+    little they weigh (in fp16 down to 2^-32 of the largest) is not lost."""
+    q, k, v, scale = _one_key_and_many_far_ones(dtype, d, 1, m, gap, far)
+    o, refs = _attend(q, [k], [v], [1], scale=scale)
+    for rows, want, tol in refs:
+        assert_close(o[rows], want, tol)
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("new", [1, 4])
+@pytest.mark.parametrize("gap", [0, 3, 30])
+def test_values_that_are_not_finite_and_seen_by_all(dtype, value, new, gap):
+    """An infinite value seen by every row, in the middle of a long cache and at its end, under a weight that
+    is exactly a power of two and however small: the column is that infinity, or NaN, and no other is."""
+    q, k, v, scale = _one_key_and_many_far_ones(dtype, 128, new, 700, gap, 2.0)
+    for j, c in ((5, 7), (333, 8), (695, 100)):
+        v[j, 0, c] = value
+    v[40, 0, 8] = -value
+    o, refs = _attend(q, [k], [v], [new], scale=scale, causal=False)
+    for rows, want, tol in refs:
+        assert_close(o[rows], want, tol)
