@@ -421,7 +421,8 @@ int lite_attn_gqa_workspace(lite_attn_gqa_t plan, int B, int64_t tokens, int max
 /* New tokens into the cache.
  *   k, v     : the new keys and values, `tokens` rows of Hk heads.
  *   q, q_out : queries to rotate beside them, Hq heads (ptr NULL: none);
- *              q_out == q rotates in place.
+ *              q_out == q rotates in place (k and v may then be other slices of
+ *              the same projection, but share no element with q).
  *   k_pages, v_pages : the cache, `pages` pages of `page` tokens (a power of
  *              two from 16 to 65536), each [pages][Hk][page][d]
  *              (LITE_LAYOUT_BHND) or [pages][page][Hk][d] (LITE_LAYOUT_BNHD).

@@ -3,9 +3,11 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -56,6 +58,29 @@ size_t rows_bytes(const lite_attn_rows_t &r, int heads, int d) {
 bool apart(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return na == 0 || nb == 0 || x + na <= y || y + nb <= x;
+}
+// Whether two views of the same number of tokens share an element.  Slices of one projection may lie
+// between one another's rows (or heads); of other views whose ranges meet it is taken that they do.
+bool share_elements(const lite_attn_rows_t &a, int heads_a, const lite_attn_rows_t &b, int heads_b, int d) {
+    if (apart(a.ptr, rows_bytes(a, heads_a, d), b.ptr, rows_bytes(b, heads_b, d))) return false;
+    const int64_t last = a.tokens - 1, step = a.stride_token;
+    if (last > 0 && b.stride_token != step) return true;
+    const int64_t base = (reinterpret_cast<intptr_t>(b.ptr) - reinterpret_cast<intptr_t>(a.ptr)) / 2;
+    auto meet = [&](int64_t off) {   // rows of d elements, `off` apart in the same token: in any two tokens
+        int64_t n = std::max(-last, std::min(last, -off / step));
+        for (int64_t k = std::max(-last, n - 1); k <= std::min(last, n + 1); ++k)
+            if (std::abs(off + k * step) < d) return true;
+        return false;
+    };
+    if (a.stride_head == b.stride_head) {
+        for (int64_t e = 1 - heads_a; e < heads_b; ++e)
+            if (meet(base + e * a.stride_head)) return true;
+    } else {
+        for (int64_t i = 0; i < heads_a; ++i)
+            for (int64_t j = 0; j < heads_b; ++j)
+                if (meet(base + j * b.stride_head - i * a.stride_head)) return true;
+    }
+    return false;
 }
 
 struct CacheView {
@@ -436,7 +461,7 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *a, vo
         const size_t nb = static_cast<size_t>(a->angle_rows) * (a->rot / 2) * 4u;
         if (!device_range_ok(a->cos, nb, dev) || !device_range_ok(a->sin, nb, dev)) return LITE_ERR_INVALID_ARG;
     }
-    // the outputs overlap no input and not one another; q may be rotated in place
+    // the outputs overlap no input and not one another; q may be rotated in place, k and v between its rows then
     const size_t cb = cache_bytes(plan, c);
     const lite_attn_rows_t *in[3] = {&a->k, &a->v, &a->q};
     const bool in_place = has_q && a->q.ptr == a->q_out.ptr && a->q.stride_token == a->q_out.stride_token &&
@@ -444,6 +469,7 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *a, vo
     for (int i = 0; i < (has_q ? 3 : 2); ++i) {
         const size_t nb = rows_bytes(*in[i], i == 2 ? plan->Hq : plan->Hk, d);
         if (!apart(in[i]->ptr, nb, c.k, cb) || !apart(in[i]->ptr, nb, c.v, cb)) return LITE_ERR_INVALID_ARG;
+        if (has_q && in_place && i < 2 && share_elements(a->q_out, plan->Hq, *in[i], plan->Hk, d)) return LITE_ERR_INVALID_ARG;
         if (has_q && !in_place && !apart(in[i]->ptr, nb, a->q_out.ptr, rows_bytes(a->q_out, plan->Hq, d)))
             return LITE_ERR_INVALID_ARG;
     }

@@ -126,3 +126,62 @@ def _allocator_child():
 @pytest.mark.parametrize("conf", ["expandable_segments:False", "expandable_segments:True", "backend:cudaMallocAsync"])
 def test_memory_of_other_allocators(conf):
     _other_allocator(conf)
+
+
+# ---------------------------------------------------------------- inputs and outputs in one another's memory
+def _append_args(T=6, Hq=4, Hk=2, d=64, dtype=BF16):
+    from temporal_block_sparse_sm_b200 import serving
+    plan = serving.GroupedPlan(Hq, Hk, d, dtype=dtype)
+    pools = [torch.zeros(2, Hk, 16, d, dtype=dtype, device="cuda") for _ in range(2)]
+    cos, sin = serving.rotation_table(range(40), [0.3 * i + 0.1 for i in range(d // 2)], device="cuda")
+    return plan, serving.PagedCache(plan, *pools), pools, dict(lens=_ints(T), cu_new=offsets([T]), table=_ints(1, 0).view(1, 2), cos=cos, sin=sin)
+
+
+def test_queries_rotated_in_place_must_not_be_keys_or_values():
+    """q_out == q, and k or v reads some of the elements that are written."""
+    from temporal_block_sparse_sm_b200 import liteattn
+    plan, cache, pools, kw = _append_args()
+    x = _randn(9, 8, 64)
+    q, other = x[1:7, 1:5], _randn(6, 2, 64)
+    per_head = _randn(6, 4, 2, 64)                # [token][head][a, b]
+    heads_first = _randn(4, 8, 64).transpose(0, 1)
+    cases = [(q, x[1:7, 1:3]), (q, x[1:7, 4:6]), (q, x[1:7, 0:2]), (q, x[2:8, 3:5]), (q, x[0:6, 2:4]),
+             (q, x[1:7, 0:8:4]), (per_head[:, :, 0], per_head[:, 1:3, 0]), (heads_first[:6], heads_first[2:, 1:3]),
+             (q, x.flatten()[512 + 320 - 32:].as_strided((6, 2, 64), (512, 64, 1))),
+             (q, x.flatten()[512 + 64:].as_strided((6, 2, 64), (384, 64, 1)))]
+    before = liteattn.lite_attn_launch_count()
+    for i, (a, b) in enumerate(cases):
+        for k, v in ((b, other), (other, b)):
+            with pytest.raises(liteattn.LiteAttnError) as e:
+                cache.append(k, v, q=a, q_out=a, **kw)
+            assert e.value.code == liteattn.LITE_ERR_INVALID_ARG, i
+    assert liteattn.lite_attn_launch_count() == before
+
+
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("form", ["fused", "per head", "heads first", "apart", "pieces of a wide row"])
+def test_queries_rotated_in_place_between_keys_and_values(form, T):
+    """The same elements' neighbours are fine: slices of one projection, whatever their order in it."""
+    Hq, Hk, d = (4, 4, 64) if form == "per head" else (4, 2, 64)
+    plan, cache, pools, kw = _append_args(T, Hq, Hk)
+    if form == "fused":
+        q, k, v = _randn(T, Hq + 2 * Hk, d).split([Hq, Hk, Hk], dim=1)
+    elif form == "per head":
+        q, k, v = _randn(T, Hq, 3, d).unbind(2)
+    elif form == "heads first":
+        q, k, v = _randn(Hq + 2 * Hk, T, d).transpose(0, 1).split([Hq, Hk, Hk], dim=1)
+    elif form == "apart":
+        q, k, v = (_randn(T, h, d, seed=h + i) for i, h in enumerate((Hq, Hk, Hk)))
+    else:
+        x = _randn(T, 40, d)
+        k, q, v = x[:, 3:3 + Hk], x[:, 10:10 + 3 * Hq:3], x[:, 11:11 + 4 * Hk:6][:, :Hk]
+    want_q, saved = torch.empty(T, Hq, d, dtype=BF16, device="cuda"), (q.clone(), k.clone(), v.clone())
+    cache.append(k, v, q=saved[0], q_out=want_q, **kw)
+    want_pools = [p.clone() for p in pools]
+    for p in pools:
+        p.zero_()
+    cache.append(k, v, q=q, q_out=q, **kw)
+    plan.check()
+    assert torch.equal(q, want_q) and torch.equal(k, saved[1]) and torch.equal(v, saved[2])
+    assert all(torch.equal(a, b) for a, b in zip(pools, want_pools))
+    assert torch.equal(q, saved[0]) == (T == 1)        # position 0 turns by angles of 0: cos 1, sin 0
