@@ -464,7 +464,8 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *args,
  *              attends to all of itself); otherwise as above.
  *   scale    : factor of the logits, > 0 (1 / sqrt(d) usually).
  *   workspace: device scratch of lite_attn_gqa_workspace bytes, 16-byte
- *              aligned; free for reuse in stream order.
+ *              aligned, overlapping nothing else of the call; free for reuse in
+ *              stream order.
  * Errors: INVALID_ARG, UNSUPPORTED (over 2^30 keys, 2^31 query rows), CUDA; on the
  * device: LITE_ERR_DEVICE_CHECK, LITE_ERR_DEVICE_TIMEOUT. */
 typedef struct {

@@ -306,7 +306,14 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     if (dv.items >= (int64_t(1) << 31) || dv.blocks > kJoinThreads) return LITE_ERR_UNSUPPORTED;
     if (workspace_bytes < dv.workspace) return LITE_ERR_INVALID_ARG;
     if (dv.workspace && !device_range_ok(workspace, dv.workspace, pl->device)) return LITE_ERR_INVALID_ARG;
-    if (dv.workspace && !apart(workspace, dv.workspace, o.ptr, rows_bytes(o, pl->Hq, pl->d))) return LITE_ERR_INVALID_ARG;
+    if (dv.workspace) {    // overlaps nothing else that the call reads or writes
+        const void *used[7] = {o.ptr, q.ptr, c ? c->k : k->ptr, c ? c->v : v->ptr, b.cu_q, c ? b.lens : b.cu_k, b.table};
+        const size_t kv = c ? cache_bytes(pl, *c) : 0, ints = 4u * static_cast<size_t>(b.B);
+        const size_t bytes[7] = {rows_bytes(o, pl->Hq, pl->d), rows_bytes(q, pl->Hq, pl->d), c ? kv : rows_bytes(*k, pl->Hk, pl->d),
+                                 c ? kv : rows_bytes(*v, pl->Hk, pl->d), ints + 4u, c ? ints : ints + 4u, c ? ints * b.table_w : 0};
+        for (int i = 0; i < 7; ++i)
+            if (!apart(workspace, dv.workspace, used[i], bytes[i])) return LITE_ERR_INVALID_ARG;
+    }
     if (fault("launch")) return LITE_ERR_CUDA;
     b.G = G;
     b.Hk = pl->Hk;

@@ -185,3 +185,62 @@ def test_queries_rotated_in_place_between_keys_and_values(form, T):
     assert torch.equal(q, want_q) and torch.equal(k, saved[1]) and torch.equal(v, saved[2])
     assert all(torch.equal(a, b) for a, b in zip(pools, want_pools))
     assert torch.equal(q, saved[0]) == (T == 1)        # position 0 turns by angles of 0: cos 1, sin 0
+
+
+def _rows(t):
+    from temporal_block_sparse_sm_b200 import liteattn
+    return liteattn.Rows(t.data_ptr(), t.shape[0], t.stride(0), t.stride(1))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("call", ["attend", "prompt"])
+def test_a_workspace_over_other_arguments_is_refused(call, new):
+    """Through the C ABI's binding, with a workspace in an allocation that holds an argument as well: behind
+    it, which is fine, and reaching into it from either side."""
+    import ctypes
+
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    Hq, Hk, d, m, page, pages = 4, 1, 64, 20000, 64, 320
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    bytes_ = liteattn.lite_attn_gqa_workspace(plan.handle, 1, new, new, pages * page if call == "attend" else m)
+    assert bytes_ > 0
+    made = dict(q=_randn(new, Hq, d), o=torch.full((new, Hq, d), 7.0, dtype=BF16, device="cuda"), cu_q=offsets([new]))
+    if call == "attend":
+        made.update(k=_randn(pages, Hk, page, d), v=_randn(pages, Hk, page, d, seed=1), lens=_ints(m),
+                    table=torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages))
+    else:
+        made.update(k=_randn(m, Hk, d), v=_randn(m, Hk, d, seed=1), cu_k=offsets([m]))
+
+    def run(t, ws):
+        if call == "attend":
+            args = liteattn.AttendArgs(q=_rows(t["q"]), o=_rows(t["o"]), k_pages=t["k"].data_ptr(), v_pages=t["v"].data_ptr(), pages=pages,
+                                       cu_new=t["cu_q"].data_ptr(), lens=t["lens"].data_ptr(), table=t["table"].data_ptr(), workspace=ws,
+                                       workspace_bytes=bytes_, B=1, table_width=pages, page=page, layout=0, max_new=new, causal=1, scale=0.125)
+            liteattn.lite_attn_cache_attend(plan.handle, ctypes.addressof(args))
+        else:
+            args = liteattn.PromptArgs(q=_rows(t["q"]), o=_rows(t["o"]), k=_rows(t["k"]), v=_rows(t["v"]), cu_q=t["cu_q"].data_ptr(),
+                                       cu_k=t["cu_k"].data_ptr(), workspace=ws, workspace_bytes=bytes_, B=1, causal=1, scale=0.125)
+            liteattn.lite_attn_prompt(plan.handle, ctypes.addressof(args))
+
+    own = torch.empty(bytes_, dtype=torch.uint8, device="cuda")
+    run(made, own.data_ptr())
+    plan.check()
+    want = made["o"].clone()
+    for name, t in made.items():
+        size = -(-t.numel() * t.element_size() // 256) * 256
+        pad = -(-bytes_ // 256) * 256
+        flat = torch.zeros(2 * pad + size, dtype=torch.uint8, device="cuda")
+        inside = flat[pad:pad + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        inside.copy_(t)
+        moved = dict(made, **{name: inside})
+        used = t.numel() * t.element_size()
+        run(moved, flat.data_ptr() + pad + size)
+        run(moved, flat.data_ptr() + pad - (bytes_ + 15) // 16 * 16)
+        plan.check()
+        assert torch.equal(moved["o"], want), name
+        before = liteattn.lite_attn_launch_count()
+        for at in (pad - (bytes_ - 1) // 16 * 16, pad, pad + (used - 1) // 16 * 16):
+            with pytest.raises(liteattn.LiteAttnError) as e:
+                run(moved, flat.data_ptr() + at)
+            assert e.value.code == liteattn.LITE_ERR_INVALID_ARG, (name, at)
+        assert liteattn.lite_attn_launch_count() == before
