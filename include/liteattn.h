@@ -462,7 +462,7 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *args,
  *              host; it only selects between kernels (any value is correct).
  *   causal   : 0: every new token sees all of its sequence's keys (a frame that
  *              attends to all of itself); otherwise as above.
- *   scale    : factor of the logits, > 0 (1 / sqrt(d) usually).
+ *   scale    : factor of the logits, > 0 and below 2.35e38 (1 / sqrt(d) usually).
  *   workspace: device scratch of lite_attn_gqa_workspace bytes, 16-byte
  *              aligned, overlapping nothing else of the call; free for reuse in
  *              stream order.

@@ -46,6 +46,9 @@ bool rows_ok(const lite_attn_rows_t &r, int heads, int d, int device) {
     const size_t elems = static_cast<size_t>(r.tokens - 1) * r.stride_token + static_cast<size_t>(heads - 1) * r.stride_head + d;
     return device_range_ok(r.ptr, elems * 2u, device);
 }
+// The kernels' factor of the logits: to the base 2, in 32 bits.
+float scale_log2(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634); }
+bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale_log2(scale)); }
 // An output's rows lie apart: whole tokens behind one another, or whole heads.
 bool rows_apart(const lite_attn_rows_t &r, int heads, int d) {
     return r.tokens == 0 || r.stride_token >= static_cast<int64_t>(heads - 1) * r.stride_head + d ||
@@ -334,7 +337,7 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     p.q = static_cast<const uint16_t *>(q.ptr);
     p.o = static_cast<uint16_t *>(o.ptr);
     p.q_st = q.stride_token, p.q_sh = q.stride_head, p.o_st = o.stride_token, p.o_sh = o.stride_head;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.scale_log2 = scale_log2(scale);
     if (dv.split) {
         const size_t rows = 2 * static_cast<size_t>(dv.blocks) * dv.rows;
         p.ws_o = static_cast<float *>(workspace);
@@ -520,7 +523,7 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *a, vo
 int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *a, void *stream) {
     if (!valid_gqa(plan) || !a || a->B < 0 || a->table_width < 1 || a->max_new < 0)
         return LITE_ERR_INVALID_ARG;
-    if (!(a->scale > 0.0f) || std::isinf(a->scale) || a->q.tokens != a->o.tokens) return LITE_ERR_INVALID_ARG;
+    if (!scale_ok(a->scale) || a->q.tokens != a->o.tokens) return LITE_ERR_INVALID_ARG;
     const int dev = plan->device, d = plan->d;
     const CacheView c{a->k_pages, a->v_pages, a->pages, a->page, a->layout};
     DeviceScope ds(dev);
@@ -552,7 +555,7 @@ int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *a, vo
 
 int lite_attn_prompt(lite_attn_gqa_t plan, const lite_attn_prompt_t *a, void *stream) {
     if (!valid_gqa(plan) || !a || a->B < 0) return LITE_ERR_INVALID_ARG;
-    if (!(a->scale > 0.0f) || std::isinf(a->scale) || a->q.tokens != a->o.tokens || a->k.tokens != a->v.tokens)
+    if (!scale_ok(a->scale) || a->q.tokens != a->o.tokens || a->k.tokens != a->v.tokens)
         return LITE_ERR_INVALID_ARG;
     const int dev = plan->device, d = plan->d;
     DeviceScope ds(dev);

@@ -7,7 +7,7 @@ import threading
 import pytest
 import torch
 
-from tests.serving_ref import offsets
+from tests.serving_ref import assert_close, offsets, seq_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -98,7 +98,7 @@ def _allocator_child():
     import math
 
     from temporal_block_sparse_sm_b200 import liteattn, serving
-    from tests.serving_ref import assert_close, seq_reference
+
     Hq, Hk, d, page, n, pages = 8, 2, 128, 64, 300, 4096           # pools of 134 MB
     q, k, v = (_randn(n, h, d, seed=i) for i, h in enumerate((Hq, Hk, Hk)))
     plan = serving.GroupedPlan(Hq, Hk, d)
@@ -244,3 +244,25 @@ def test_a_workspace_over_other_arguments_is_refused(call, new):
                 run(moved, flat.data_ptr() + at)
             assert e.value.code == liteattn.LITE_ERR_INVALID_ARG, (name, at)
         assert liteattn.lite_attn_launch_count() == before
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_scales_at_the_end_of_the_range(new):
+    """The kernels' factor is scale * log2 e: a scale whose factor is no 32-bit number is refused, and the
+    largest others give what they say on logits that are 0 or small."""
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    plan, Hq, Hk, d = serving.GroupedPlan(4, 2, 64), 4, 2, 64
+    q, k, v = torch.zeros(new, Hq, d, dtype=BF16, device="cuda"), _randn(200, Hk, d), _randn(200, Hk, d, seed=1)
+    o, cu_q, cu_k = torch.empty_like(q), offsets([new]), offsets([200])
+    before = liteattn.lite_attn_launch_count()
+    for scale in (2.4e38, 3.4e38):
+        with pytest.raises(liteattn.LiteAttnError) as e:
+            plan.prompt(q, k, v, o, cu_q, cu_k, scale=scale)
+        assert e.value.code == liteattn.LITE_ERR_INVALID_ARG
+    assert liteattn.lite_attn_launch_count() == before
+    for factor, scale in ((0.0, 2.3e38), (2.0 ** -120, 2.0 ** 117), (2.0 ** -120, 2.0 ** 120)):
+        q.fill_(factor)
+        plan.prompt(q, k, v, o, cu_q, cu_k, scale=scale, causal=False)
+        plan.check()
+        want, tol = seq_reference(q, k, v, False, scale)
+        assert_close(o, want, tol, f"scale {scale}")
