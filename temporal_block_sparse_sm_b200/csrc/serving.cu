@@ -62,6 +62,17 @@ bool apart(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return na == 0 || nb == 0 || x + na <= y || y + nb <= x;
 }
+// A stretch of memory that a call reads.
+struct Input {
+    const void *ptr;
+    size_t bytes;
+};
+template <int N>
+bool apart_from(const void *out, size_t bytes, const Input (&in)[N]) {
+    for (const Input &x : in)
+        if (!apart(out, bytes, x.ptr, x.bytes)) return false;
+    return true;
+}
 // Whether two views of the same number of tokens share an element.  Slices of one projection may lie
 // between one another's rows (or heads); of other views whose ranges meet it is taken that they do.
 bool share_elements(const lite_attn_rows_t &a, int heads_a, const lite_attn_rows_t &b, int heads_b, int d) {
@@ -310,12 +321,12 @@ int attention(lite_attn_gqa *pl, const CacheView *c, const lite_attn_rows_t *k, 
     if (workspace_bytes < dv.workspace) return LITE_ERR_INVALID_ARG;
     if (dv.workspace && !device_range_ok(workspace, dv.workspace, pl->device)) return LITE_ERR_INVALID_ARG;
     if (dv.workspace) {    // overlaps nothing else that the call reads or writes
-        const void *used[7] = {o.ptr, q.ptr, c ? c->k : k->ptr, c ? c->v : v->ptr, b.cu_q, c ? b.lens : b.cu_k, b.table};
         const size_t kv = c ? cache_bytes(pl, *c) : 0, ints = 4u * static_cast<size_t>(b.B);
-        const size_t bytes[7] = {rows_bytes(o, pl->Hq, pl->d), rows_bytes(q, pl->Hq, pl->d), c ? kv : rows_bytes(*k, pl->Hk, pl->d),
-                                 c ? kv : rows_bytes(*v, pl->Hk, pl->d), ints + 4u, c ? ints : ints + 4u, c ? ints * b.table_w : 0};
-        for (int i = 0; i < 7; ++i)
-            if (!apart(workspace, dv.workspace, used[i], bytes[i])) return LITE_ERR_INVALID_ARG;
+        const Input used[7] = {{o.ptr, rows_bytes(o, pl->Hq, pl->d)}, {q.ptr, rows_bytes(q, pl->Hq, pl->d)},
+                               {c ? c->k : k->ptr, c ? kv : rows_bytes(*k, pl->Hk, pl->d)},
+                               {c ? c->v : v->ptr, c ? kv : rows_bytes(*v, pl->Hk, pl->d)}, {b.cu_q, ints + 4u},
+                               {c ? b.lens : b.cu_k, c ? ints : ints + 4u}, {b.table, c ? ints * b.table_w : 0}};
+        if (!apart_from(workspace, dv.workspace, used)) return LITE_ERR_INVALID_ARG;
     }
     if (fault("launch")) return LITE_ERR_CUDA;
     b.G = G;
@@ -483,10 +494,13 @@ int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *a, vo
         if (has_q && !in_place && !apart(in[i]->ptr, nb, a->q_out.ptr, rows_bytes(a->q_out, plan->Hq, d)))
             return LITE_ERR_INVALID_ARG;
     }
-    if (has_q) {
-        const size_t nb = rows_bytes(a->q_out, plan->Hq, d);
-        if (!apart(a->q_out.ptr, nb, c.k, cb) || !apart(a->q_out.ptr, nb, c.v, cb)) return LITE_ERR_INVALID_ARG;
-    }
+    const size_t ob = has_q ? rows_bytes(a->q_out, plan->Hq, d) : 0, ints = 4u * static_cast<size_t>(a->B);
+    const size_t ab = a->cos ? static_cast<size_t>(a->angle_rows) * (a->rot / 2) * 4u : 0;
+    const Input fixed[6] = {{a->cos, ab}, {a->sin, ab}, {a->positions, a->positions ? 4u * static_cast<size_t>(a->k.tokens) : 0},
+                            {a->cu_new, ints + 4u}, {a->lens, ints}, {a->table, ints * a->table_width}};
+    if (!apart(a->q_out.ptr, ob, c.k, cb) || !apart(a->q_out.ptr, ob, c.v, cb) || !apart_from(a->q_out.ptr, ob, fixed) ||
+        !apart_from(c.k, cb, fixed) || !apart_from(c.v, cb, fixed))
+        return LITE_ERR_INVALID_ARG;
     if (fault("launch")) return LITE_ERR_CUDA;
     NvtxRange range("lite_attn_cache_append");
 
@@ -538,10 +552,10 @@ int lite_attn_cache_attend(lite_attn_gqa_t plan, const lite_attn_attend_t *a, vo
     if (!ints_ok(a->cu_new, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->lens, a->B, dev) ||
         !ints_ok(a->table, static_cast<size_t>(a->B) * a->table_width, dev))
         return LITE_ERR_INVALID_ARG;
-    const size_t ob = rows_bytes(a->o, plan->Hq, d), cb = cache_bytes(plan, c);
-    if (!apart(a->o.ptr, ob, a->q.ptr, rows_bytes(a->q, plan->Hq, d)) || !apart(a->o.ptr, ob, c.k, cb) ||
-        !apart(a->o.ptr, ob, c.v, cb))
-        return LITE_ERR_INVALID_ARG;
+    const size_t cb = cache_bytes(plan, c), ints = 4u * static_cast<size_t>(a->B);
+    const Input in[6] = {{a->q.ptr, rows_bytes(a->q, plan->Hq, d)}, {c.k, cb}, {c.v, cb}, {a->cu_new, ints + 4u}, {a->lens, ints},
+                         {a->table, ints * a->table_width}};
+    if (!apart_from(a->o.ptr, rows_bytes(a->o, plan->Hq, d), in)) return LITE_ERR_INVALID_ARG;
     NvtxRange range("lite_attn_cache_attend");
     GqaBatch b;
     std::memset(&b, 0, sizeof b);
@@ -567,10 +581,10 @@ int lite_attn_prompt(lite_attn_gqa_t plan, const lite_attn_prompt_t *a, void *st
         return LITE_ERR_INVALID_ARG;
     if (!ints_ok(a->cu_q, static_cast<size_t>(a->B) + 1, dev) || !ints_ok(a->cu_k, static_cast<size_t>(a->B) + 1, dev))
         return LITE_ERR_INVALID_ARG;
-    const size_t ob = rows_bytes(a->o, plan->Hq, d);
-    if (!apart(a->o.ptr, ob, a->q.ptr, rows_bytes(a->q, plan->Hq, d)) || !apart(a->o.ptr, ob, a->k.ptr, rows_bytes(a->k, plan->Hk, d)) ||
-        !apart(a->o.ptr, ob, a->v.ptr, rows_bytes(a->v, plan->Hk, d)))
-        return LITE_ERR_INVALID_ARG;
+    const size_t ints = 4u * static_cast<size_t>(a->B) + 4u;
+    const Input in[5] = {{a->q.ptr, rows_bytes(a->q, plan->Hq, d)}, {a->k.ptr, rows_bytes(a->k, plan->Hk, d)},
+                         {a->v.ptr, rows_bytes(a->v, plan->Hk, d)}, {a->cu_q, ints}, {a->cu_k, ints}};
+    if (!apart_from(a->o.ptr, rows_bytes(a->o, plan->Hq, d), in)) return LITE_ERR_INVALID_ARG;
     NvtxRange range("lite_attn_prompt");
     GqaBatch b;
     std::memset(&b, 0, sizeof b);

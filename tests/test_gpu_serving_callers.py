@@ -266,3 +266,42 @@ def test_scales_at_the_end_of_the_range(new):
         plan.check()
         want, tol = seq_reference(q, k, v, False, scale)
         assert_close(o, want, tol, f"scale {scale}")
+
+
+def test_outputs_over_lengths_offsets_tables_and_angles_are_refused():
+    from temporal_block_sparse_sm_b200 import liteattn, serving
+    Hq, Hk, d, T = 4, 2, 64, 6
+    plan, cache, pools, kw = _append_args(T)
+    q, k, v = (_randn(T, h, d, seed=h + i) for i, h in enumerate((Hq, Hk, Hk)))
+    kw["positions"] = torch.zeros(T, dtype=torch.int32, device="cuda")
+    before = liteattn.lite_attn_launch_count()
+
+    def within(host, t):
+        """t's values in the memory of host, somewhere in its middle."""
+        flat = host.flatten().view(torch.uint8)
+        at = flat.numel() // 2 // 16 * 16
+        out = flat[at:at + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        out.copy_(t)
+        return out
+
+    for name in ("lens", "cu_new", "table", "positions"):
+        out = torch.zeros(T, Hq, d, dtype=BF16, device="cuda")
+        for host in (out, pools[0], pools[1]):
+            with pytest.raises(liteattn.LiteAttnError) as e:
+                cache.append(k, v, q=q, q_out=out, **dict(kw, **{name: within(host, kw[name])}))
+            assert e.value.code == liteattn.LITE_ERR_INVALID_ARG, name
+        if name != "positions":
+            args = dict(lens=kw["lens"], cu_new=kw["cu_new"], table=kw["table"])
+            with pytest.raises(liteattn.LiteAttnError):
+                cache.attend(q, out, max_new=T, **dict(args, **{name: within(out, kw[name])}))
+    wide = torch.zeros(64, Hq, d, dtype=BF16, device="cuda")
+    for name in ("cos", "sin"):
+        with pytest.raises(liteattn.LiteAttnError):
+            cache.append(_randn(64, Hk, d), _randn(64, Hk, d), q=_randn(64, Hq, d), q_out=wide,
+                         **dict(kw, lens=_ints(32), cu_new=offsets([32]), positions=torch.zeros(64, dtype=torch.int32, device="cuda"),
+                                **{name: within(wide, kw[name])}))
+    out = torch.zeros(T, Hq, d, dtype=BF16, device="cuda")
+    for name in ("cu_q", "cu_k"):
+        with pytest.raises(liteattn.LiteAttnError):
+            plan.prompt(q, k, v, out, **dict(dict(cu_q=offsets([T]), cu_k=offsets([T])), **{name: within(out, offsets([T]))}))
+    assert liteattn.lite_attn_launch_count() == before
