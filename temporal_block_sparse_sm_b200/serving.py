@@ -159,18 +159,29 @@ class PagedCache:
         if layout not in _c._LAYOUTS:
             raise ValueError(f"layout must be one of {sorted(_c._LAYOUTS)}")
         self.plan, self.k_pages, self.v_pages, self.layout = plan, k_pages, v_pages, layout
+        self._layout = _c._LAYOUTS[layout]
+        self._pool = self._check_pages()
+
+    def _check_pages(self):
+        """(addresses, number) of the pages, after a look at the tensors."""
+        plan, k_pages, v_pages = self.plan, self.k_pages, self.v_pages
         for t, nm in ((k_pages, "k_pages"), (v_pages, "v_pages")):
             if t.dim() != 4 or not t.is_cuda or t.dtype != plan.dtype or not t.is_contiguous() or t.shape != k_pages.shape:
                 raise ValueError(f"{nm} must be a contiguous CUDA tensor of {plan.dtype} with four dimensions")
-        self.pages = k_pages.shape[0]
-        heads, page = (1, 2) if layout == "bhnd" else (2, 1)
+        heads, page = (1, 2) if self.layout == "bhnd" else (2, 1)
         if k_pages.shape[heads] != plan.Hk or k_pages.shape[3] != plan.d:
             raise ValueError(f"the pages must hold {plan.Hk} heads of {plan.d}")
-        self.page = k_pages.shape[page]
+        self.pages, self.page = k_pages.shape[0], k_pages.shape[page]
         if self.page < 16 or self.page & (self.page - 1):
             raise ValueError("a page must hold a power of two of tokens, 16 or more")
-        self._pool = (k_pages.data_ptr(), v_pages.data_ptr(), self.pages)
-        self._layout = _c._LAYOUTS[layout]
+        return k_pages.data_ptr(), v_pages.data_ptr(), self.pages
+
+    def _pages(self):
+        """The pages where they are now: the tensors are the caller's, who may give them other memory."""
+        pool = self._pool
+        if self.k_pages.data_ptr() != pool[0] or self.v_pages.data_ptr() != pool[1]:
+            pool = self._pool = self._check_pages()
+        return pool
 
     def append(self, k, v, lens, cu_new, table, q=None, q_out=None, cos=None, sin=None, positions=None,
                interleaved: bool = False, stream=None):
@@ -199,8 +210,8 @@ class PagedCache:
             if rot % 16 or not 16 <= rot <= p.d:
                 raise ValueError("rot must be a multiple of 16, at most d")
             a = (cos.data_ptr(), sin.data_ptr(), rows)
-        B, width = cu_new.numel() - 1, table.shape[-1]
-        args = _APPEND.pack(*rq, *ro, *rk, *rv, *self._pool, *a,
+        B, width, pool = cu_new.numel() - 1, table.shape[-1], self._pages()
+        args = _APPEND.pack(*rq, *ro, *rk, *rv, *pool, *a,
                             p._ints(positions, rk[1], "positions") if positions is not None else 0,
                             p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),
                             p._ints(table, B * width, "table"), B, width, self.page, self._layout, rot, 1 if interleaved else 0)
@@ -215,13 +226,13 @@ class PagedCache:
         host; it selects the kernel.  causal=False: every new token sees all keys of its
         sequence."""
         p = self.plan
-        rq, ro = p._rows(q, p.Hq, "q"), p._rows(o, p.Hq, "o")
+        rq, ro, pool = p._rows(q, p.Hq, "q"), p._rows(o, p.Hq, "o"), self._pages()
         B, width = cu_new.numel() - 1, table.shape[-1]
         if max_new > rq[1]:
             max_new = rq[1]
         s = p._stream(stream)
         w = p._workspace(B, rq[1], max_new, width * self.page, s)
-        args = _ATTEND.pack(*rq, *ro, *self._pool, p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),
+        args = _ATTEND.pack(*rq, *ro, *pool, p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),
                             p._ints(table, B * width, "table"), w.data_ptr() if w is not None else 0,
                             w.shape[0] if w is not None else 0, B, width, self.page, self._layout, max_new,
                             1 if causal else 0, p._scale(scale), 0)

@@ -305,3 +305,42 @@ def test_outputs_over_lengths_offsets_tables_and_angles_are_refused():
         with pytest.raises(liteattn.LiteAttnError):
             plan.prompt(q, k, v, out, **dict(dict(cu_q=offsets([T]), cu_k=offsets([T])), **{name: within(out, offsets([T]))}))
     assert liteattn.lite_attn_launch_count() == before
+
+
+@pytest.mark.parametrize("way", ["data", "attribute", "set_"])
+def test_pages_that_get_other_memory(way):
+    """The caller's page tensors move to other memory (with another number of pages) after the cache was made:
+    calls go to where they are; tensors that are no pages of this plan any more are refused."""
+    from temporal_block_sparse_sm_b200 import serving
+    Hq, Hk, d, T = 4, 2, 64, 20
+    q, k, v = (_randn(T, h, d, seed=h + i) for i, h in enumerate((Hq, Hk, Hk)))
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    first, fresh, wrong = ([torch.zeros(*s, dtype=BF16, device="cuda") for _ in range(2)] for s in ((8, Hk, 16, d), (3, Hk, 32, d), (8, Hk, 16, 2 * d)))
+    cache = serving.PagedCache(plan, *first)
+    lens, cu, o = _ints(T), offsets([T]), [torch.empty_like(q) for _ in range(2)]
+    cache.append(k, v, lens, cu, _ints(7, 2).view(1, 2))
+    cache.attend(q, o[0], lens, cu, _ints(7, 2).view(1, 2), max_new=T)
+    plan.check()
+    kept, old = [x.clone() for x in first], [x.detach() for x in first]
+
+    def move(tensors):
+        for name, x in zip(("k_pages", "v_pages"), tensors):
+            if way == "attribute":
+                setattr(cache, name, x)
+            elif way == "data":
+                getattr(cache, name).data = x
+            else:
+                getattr(cache, name).set_(x)
+    move(fresh)
+    cache.append(k, v, lens, cu, _ints(2).view(1, 1))
+    cache.attend(q, o[1], lens, cu, _ints(2).view(1, 1), max_new=T)
+    plan.check()
+    want, tol = seq_reference(q, k, v, True, d ** -0.5)
+    for x in o:
+        assert_close(x, want, tol)
+    assert all(torch.equal(a, b) for a, b in zip(old, kept)), "the memory of before was written"
+    move(wrong)
+    with pytest.raises(ValueError):
+        cache.append(k, v, lens, cu, _ints(2).view(1, 1))
+    with pytest.raises(ValueError):
+        cache.attend(q, o[0], lens, cu, _ints(2).view(1, 1), max_new=T)
