@@ -63,7 +63,8 @@ enum {
     LITE_ERR_ALLOC = -4,          /* device or host allocation failed */
     LITE_ERR_CUDA = -5,           /* CUDA runtime or launch error, or no sm_100 device */
     LITE_ERR_DEVICE_TIMEOUT = -6, /* a kernel's bounded wait ran out; its outputs are invalid */
-    LITE_ERR_DEVICE_CHECK = -7    /* debug builds (LITE_DEBUG_CHECKS): a work item failed its device-side checks */
+    LITE_ERR_DEVICE_CHECK = -7    /* a kernel found device data that it cannot use: in serving calls lengths, offsets,
+                                     pages or angle rows, in debug builds (LITE_DEBUG_CHECKS) also a work item */
 };
 
 typedef struct {
@@ -375,10 +376,14 @@ int lite_attn_compact_noalloc(const uint32_t *bits, int B, int H, int N, int Br,
  *   queries are the LAST n of the sequence's m positions: query token t sees
  *   the keys 0 .. m - n + t (causal) or all m.  A row that sees no key gets
  *   zeros.  What stands in places that no row sees (NaN included) has no effect.
- * - What the kernels find wrong in device data (lengths outside the tensors,
- *   a page that does not exist, an angle row out of range) is not used as an
- *   address: the sequence or token is left out and the plan's status becomes
- *   LITE_ERR_DEVICE_CHECK (sticky; lite_attn_gqa_status).  Lengths, offsets
+ * - What the kernels find wrong in device data is not used as an address, and
+ *   the plan's status becomes LITE_ERR_DEVICE_CHECK (sticky;
+ *   lite_attn_gqa_status).  A sequence whose lengths or offsets lie outside the
+ *   tensors, or whose offsets go backwards, is left out: nothing of it is read
+ *   or written (rows that two others name get either's result).  A new token whose
+ *   slot is below 0, whose page does not exist or whose angle row is out of
+ *   range is left out of an append.  In an attention over the cache the keys
+ *   and values of a page that does not exist count as zeros.  Lengths, offsets
  *   and tables must not be written while a call that reads them runs: results
  *   are undefined then (every access stays inside the tensors even so).
  * - Logits, softmax statistics and output sums are held in 32 bits and the

@@ -409,7 +409,7 @@ const char *lite_attn_error_string(int code) {
         case LITE_ERR_ALLOC: return "allocation failed";
         case LITE_ERR_CUDA: return "CUDA error";
         case LITE_ERR_DEVICE_TIMEOUT: return "device wait timed out";
-        case LITE_ERR_DEVICE_CHECK: return "device-side check failed (debug build)";
+        case LITE_ERR_DEVICE_CHECK: return "device data that a kernel cannot use (lengths, offsets, pages, work items)";
         default: return "unknown error";
     }
 }
