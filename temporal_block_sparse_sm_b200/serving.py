@@ -63,8 +63,6 @@ class GroupedPlan:
         self._ws = {}   # workspace bytes by (B, tokens, max_new, max_keys)
         self.handle = _c.lite_attn_gqa_create(self.Hq, self.Hk, self.d,
                                               _c.LITE_DTYPE_BF16 if dtype == torch.bfloat16 else _c.LITE_DTYPE_FP16)
-        lib = _c.load()
-        self._fn = lib.lite_attn_prompt, lib.lite_attn_cache_append, lib.lite_attn_cache_attend
 
     # ------------------------------------------------------------ arguments
     # (the library checks addresses and strides; these look at what it cannot see)
@@ -128,7 +126,7 @@ class GroupedPlan:
         args = _PROMPT.pack(*rq, *ro, *rk, *rv, self._ints(cu_q, B + 1, "cu_q"), self._ints(cu_k, B + 1, "cu_k"),
                             w.data_ptr() if w is not None else 0, w.shape[0] if w is not None else 0, B,
                             1 if causal else 0, self._scale(scale), 0)
-        _c._check(self._fn[0](self.handle, args, s), "lite_attn_prompt")
+        _c.lite_attn_prompt(self.handle, args, s)
 
     def check(self, stream=None):
         """Waits for the stream and raises if a kernel of this plan reported an error."""
@@ -215,7 +213,7 @@ class PagedCache:
                             p._ints(positions, rk[1], "positions") if positions is not None else 0,
                             p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),
                             p._ints(table, B * width, "table"), B, width, self.page, self._layout, rot, 1 if interleaved else 0)
-        _c._check(p._fn[1](p.handle, args, p._stream(stream)), "lite_attn_cache_append")
+        _c.lite_attn_cache_append(p.handle, args, p._stream(stream))
 
     def attend(self, q, o, lens, cu_new, table, max_new: int, causal: bool = True, scale: Optional[float] = None,
                stream=None):
@@ -236,4 +234,4 @@ class PagedCache:
                             p._ints(table, B * width, "table"), w.data_ptr() if w is not None else 0,
                             w.shape[0] if w is not None else 0, B, width, self.page, self._layout, max_new,
                             1 if causal else 0, p._scale(scale), 0)
-        _c._check(p._fn[2](p.handle, args, s), "lite_attn_cache_attend")
+        _c.lite_attn_cache_attend(p.handle, args, s)

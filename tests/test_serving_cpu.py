@@ -129,3 +129,41 @@ def test_paged_helper_round_trip(layout):
             pg = int(table[b, j // 16])
             assert torch.equal(kp[pg, :, j % 16] if layout == "bhnd" else kp[pg, j % 16], x[j])
     assert bool(torch.isnan(kp).any()) and offsets([2, 0, 3], device="cpu").tolist() == [0, 2, 2, 5]
+
+
+def test_objects_call_the_binding_with_their_tensors(monkeypatch):
+    """GroupedPlan and PagedCache hand addresses, lengths and strides to the binding's functions."""
+    calls = []
+    for name in ("lite_attn_prompt", "lite_attn_cache_append", "lite_attn_cache_attend"):
+        monkeypatch.setattr(liteattn, name, lambda plan, args, stream=None, name=name: calls.append((name, plan, args, stream)))
+    monkeypatch.setattr(liteattn, "lite_attn_gqa_workspace", lambda *a: 0)
+    plan = object.__new__(serving.GroupedPlan)
+    plan.Hq, plan.Hk, plan.d, plan.dtype, plan.device, plan.handle, plan._ws = 4, 2, 64, torch.bfloat16, 0, 77, {}
+    plan._i32, plan._f32, plan._current = torch.int32, torch.float32, lambda device: 0
+    x = torch.zeros(9, 8, 64, dtype=torch.bfloat16)
+    q, k, v = x.split([4, 2, 2], dim=1)
+    o = torch.zeros(9, 4, 64, dtype=torch.bfloat16)
+    cu, lens, table = offsets([3, 6], "cpu"), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 5, dtype=torch.int32)
+    plan.prompt(q, k, v, o, cu, scale=0.5, stream=5)
+    cache = object.__new__(serving.PagedCache)
+    cache.plan, cache.k_pages, cache.v_pages = plan, torch.zeros(7, 2, 16, 64), torch.zeros(7, 2, 16, 64)
+    cache.pages, cache.page, cache._layout = 7, 16, liteattn.LITE_LAYOUT_BNHD
+    cache._pool = cache.k_pages.data_ptr(), cache.v_pages.data_ptr(), 7
+    cos, sin = serving.rotation_table(range(80), [1.0] * 16)
+    cache.append(k, v, lens, cu, table, q=q, q_out=q, cos=cos, sin=sin, interleaved=True, stream=6)
+    cache.attend(q, o, lens, cu, table, max_new=100, causal=False, stream=7)
+    plan.handle = None                                          # nothing to free
+    assert [(c[0], c[1], c[3]) for c in calls] == [("lite_attn_prompt", 77, 5), ("lite_attn_cache_append", 77, 6),
+                                                   ("lite_attn_cache_attend", 77, 7)]
+    args = [cls.from_buffer_copy(c[2]) for cls, c in zip((liteattn.PromptArgs, liteattn.AppendArgs, liteattn.AttendArgs), calls)]
+    rows = lambda r: (r.ptr, r.tokens, r.stride_token, r.stride_head)   # noqa: E731
+    view = lambda t: (t.data_ptr(), 9, t.stride(0), 64)                 # noqa: E731
+    assert all(rows(getattr(args[0], n)) == view(t) for n, t in (("q", q), ("k", k), ("v", v), ("o", o)))
+    assert (args[0].cu_q, args[0].cu_k, args[0].B, args[0].causal, args[0].scale) == (cu.data_ptr(), cu.data_ptr(), 2, 1, 0.5)
+    assert all(rows(getattr(args[1], n)) == view(t) for n, t in (("q", q), ("q_out", q), ("k", k), ("v", v)))
+    a = args[1]
+    assert (a.k_pages, a.v_pages, a.pages, a.page, a.layout, a.table_width) == (*cache._pool, 16, liteattn.LITE_LAYOUT_BNHD, 5)
+    assert (a.cos, a.sin, a.angle_rows, a.rot, a.interleaved, a.positions) == (cos.data_ptr(), sin.data_ptr(), 80, 32, 1, None)
+    a = args[2]
+    assert rows(a.q) == view(q) and rows(a.o) == view(o) and (a.max_new, a.causal, a.B) == (9, 0, 2)
+    assert (a.cu_new, a.lens, a.table, a.scale) == (cu.data_ptr(), lens.data_ptr(), table.data_ptr(), 0.125)
