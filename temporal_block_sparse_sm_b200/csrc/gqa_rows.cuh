@@ -362,17 +362,18 @@ gqa_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             // weights, in the place of the logits: of bf16 relative to the running reference; of fp16, whose range
             // is short, relative to the largest of these 16 keys (f brings the product into the frame of the sums)
+            // The difference of the logits first: c s - c m with c m rounded is off by 2^-24 of c m, whole powers
+            // of two for logits of 10^7 and more, which is beyond fp16's range.
             float f[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float ref = F16 ? top[r] : m_ref[r];
-                const float neg = ref == -INFINITY ? 0.0f : F16 ? fmaf(-ref, cl2, kGroupBias) : -ref * cl2;
+                const float ref = F16 ? top[r] : m_ref[r], from = ref == -INFINITY ? 0.0f : ref;
                 f[r] = !F16 ? 1.0f : ref == -INFINITY ? 0.0f : ptx::ex2(fmaf(ref - m_ref[r], cl2, -kGroupBias));
                 float sum = 0.0f;
 #pragma unroll
                 for (int nb = 0; nb < 2; ++nb) {
 #pragma unroll
-                    for (int i = 2 * r; i < 2 * r + 2; ++i) sc[nb][i] = ptx::ex2(fmaf(sc[nb][i], cl2, neg));
+                    for (int i = 2 * r; i < 2 * r + 2; ++i) sc[nb][i] = ptx::ex2(fmaf(sc[nb][i] - from, cl2, F16 ? kGroupBias : 0.0f));
                     sum += sc[nb][2 * r] + sc[nb][2 * r + 1];
                 }
                 l[r] = fmaf(sum, f[r], l[r]);

@@ -90,6 +90,11 @@ struct TileWork {
     uint32_t any_bad, bad[4][4];  // keys with values that are not finite, by tile from mask_tile on
 };
 
+// c s - c m is one operation with c m rounded before: off by 2^-24 of c m, the same for all keys of a step,
+// but not for other steps, and whole powers of two for logits of 10^7 and more, beyond fp16's
+// range.  From |c m| = kFarLogit on the difference s - m is taken first (half as many operations again).
+constexpr float kFarLogit = 4096.0f;
+
 // A value that all lanes hold, in a form that the compiler knows to be the same in all of them
 // (a reduction over the warp ends in a uniform register).  Operands of tcgen05.mma are uniform
 // registers; from values that only happen to be equal each of them is moved there before
@@ -546,6 +551,7 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             const int mine = limit - tw.t_lo * BN;    // of them from the first tile on
             float m_ref = -INFINITY, l = 0.0f;
+            bool far = false;             // the row's reference is beyond kFarLogit
             for (int u = 0; u < steps; ++u) {
                 const int buf = (seq + u) & 1;
                 const uint32_t sb = scol + buf * C::BU;
@@ -587,31 +593,62 @@ gqa_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     alpha = ptx::ex2((m_ref - m_loc) * cl2);
                     l *= alpha;
                     m_ref = m_loc;
+                    far = limit > 0 && fabsf(m_ref) * cl2 > kFarLogit;   // (rows that do not exist hold anything)
                 }
-                if (__any_sync(0xFFFFFFFFu, rescale) && ok && u > 0) {
-                    // the last step's P V may still run (this S only says that the one before it is
-                    // done); the next is issued when this step's P is handed over
-                    if (wait_all(pv_done(slot, buf ^ 1), ((s_ph >> (buf ^ 1)) & 1u) ^ 1u)) {
-                        ptx::tc_fence_after();
-                        const uint64_t a2 = ptx::f2(alpha, alpha);
+                const float from = m_ref == -INFINITY ? 0.0f : m_ref;
+                float neg = fmaf(-from, cl2, weight_bias<F16>());
+                if (__any_sync(0xFFFFFFFFu, rescale || far) && ok) {
+                    if (__any_sync(0xFFFFFFFFu, rescale) && u > 0) {
+                        // the last step's P V may still run (this S only says that the one before it is
+                        // done); the next is issued when this step's P is handed over
+                        if (wait_all(pv_done(slot, buf ^ 1), ((s_ph >> (buf ^ 1)) & 1u) ^ 1u)) {
+                            ptx::tc_fence_after();
+                            const uint64_t a2 = ptx::f2(alpha, alpha);
 #pragma unroll 1
-                        for (int ch = 0; ch < D / 16; ++ch) {
-                            uint32_t ov[16];
-                            ptx::tmem_ld16(ocol + ch * 16, ov);
-                            ptx::tmem_ld_wait16(ov);
+                            for (int ch = 0; ch < D / 16; ++ch) {
+                                uint32_t ov[16];
+                                ptx::tmem_ld16(ocol + ch * 16, ov);
+                                ptx::tmem_ld_wait16(ov);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float a, b;
-                                ptx::f2_split(ptx::mul2(ptx::f2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])), a2), a, b);
-                                ov[2 * i] = __float_as_uint(a);
-                                ov[2 * i + 1] = __float_as_uint(b);
+                                for (int i = 0; i < 8; ++i) {
+                                    float a, b;
+                                    ptx::f2_split(ptx::mul2(ptx::f2(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])), a2), a, b);
+                                    ov[2 * i] = __float_as_uint(a);
+                                    ov[2 * i + 1] = __float_as_uint(b);
+                                }
+                                ptx::tmem_st16(ocol + ch * 16, ov);
                             }
-                            ptx::tmem_st16(ocol + ch * 16, ov);
                         }
+                    }
+                    if (__any_sync(0xFFFFFFFFu, far)) {
+                        // by way of the S buffer, so that it takes few instructions (with 64 subtractions
+                        // written out here all calls were 2 to 5 % slower)
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t v[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = sc[ch >> 1][(ch & 1) * 16 + i];
+                            ptx::tmem_st16(sb + ch * 16, v);
+                        }
+                        ptx::tmem_st_wait();
+#pragma unroll 1
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t v[16];
+                            ptx::tmem_ld16(sb + ch * 16, v);
+                            ptx::tmem_ld_wait16(v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - from);
+                            ptx::tmem_st16(sb + ch * 16, v);
+                        }
+                        ptx::tmem_st_wait();
+                        ptx::tmem_ld32(sb, sc[0]);
+                        ptx::tmem_ld32(sb + 32, sc[1]);
+                        ptx::tmem_ld_wait(sc[0]);
+                        ptx::reg_tie(sc[1]);
+                        neg = weight_bias<F16>();
                     }
                 }
                 // P = 2^(c s - c m)
-                const float neg = (m_ref == -INFINITY ? 0.0f : -m_ref * cl2) + weight_bias<F16>();
                 const uint64_t n2 = ptx::f2(neg, neg);
                 uint64_t acc[4] = {};
                 // a visible logit of +inf or NaN gives a NaN weight (inf - inf), and so a NaN sum and row

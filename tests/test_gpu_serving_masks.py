@@ -95,3 +95,28 @@ def test_values_that_are_not_finite_and_seen_by_all(dtype, value, new, gap):
     o, refs = _attend(q, [k], [v], [new], scale=scale, causal=False)
     for rows, want, tol in refs:
         assert_close(o[rows], want, tol)
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("new", [1, 4, 40])
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 15, 181 * 2.0 ** 4, 181 * 2.0 ** 7, 149 * 2.0 ** 8, 171 * 2.0 ** 8, 201 * 2.0 ** 8, 233 * 2.0 ** 8, 253 * 2.0 ** 8, 214 * 2.0 ** 8])
+@pytest.mark.parametrize("where", [0, 500, 699])
+def test_logits_so_large_that_a_key_or_two_take_all(dtype, new, size, where):
+    """Logits of up to 4e8, exact in 32 bits (one product each): the keys with the largest, and no others,
+    share the weight, whatever 2^x makes of arguments this far from zero."""
+    d, m = 64, 700
+    g = _gen(5)
+    q, k = torch.zeros(new, 2, d, device="cuda"), torch.zeros(m, 1, d, device="cuda")
+    q[:, 0, 0], q[:, 1, 1] = size, -size                       # head 0 sees column 0 of k, head 1 the negative of column 1
+    k[:, 0, 0] = -size * (1 + torch.arange(m, device="cuda") % 3) / 4
+    k[:, 0, 1] = size * 0.5
+    k[where, 0, 0], k[where, 0, 1] = size, -size
+    k[100, 0, 1] = -size
+    v = torch.randn(m, 1, d, generator=g, device="cuda").to(dtype)
+    q, k = q.to(dtype), k.to(dtype)
+    o, _ = _attend(q, [k], [v], [new], scale=0.125, causal=False)
+    want = torch.stack([v[where, 0].double(), (v[where, 0].double() + v[100, 0].double()) / 2])
+    # weights and output are rounded to the type, 2^-22 of each for 2^x and the sums
+    u = torch.finfo(dtype).eps / 2
+    tol = (2 * u / (1 - u) + 2.0 ** -18) * torch.stack([v[where, 0].double().abs(), (v[where, 0].double().abs() + v[100, 0].double().abs()) / 2]) + u * want.abs()
+    assert_close(o, want.expand(new, 2, d), (tol + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps).expand(new, 2, d))
