@@ -355,17 +355,23 @@ def lite_attn_gqa_workspace(plan: int, B: int, tokens: int, max_new: int, max_ke
 
 def lite_attn_cache_append(plan: int, args, stream=None):
     """args: an AppendArgs' address, or its bytes."""
-    _check(load().lite_attn_cache_append(plan, args, _stream_ptr(stream)), "lite_attn_cache_append")
+    rc = load().lite_attn_cache_append(plan, args, stream if stream.__class__ is int else _stream_ptr(stream))
+    if rc:
+        raise LiteAttnError(rc, "lite_attn_cache_append")
 
 
 def lite_attn_cache_attend(plan: int, args, stream=None):
     """args: an AttendArgs' address, or its bytes."""
-    _check(load().lite_attn_cache_attend(plan, args, _stream_ptr(stream)), "lite_attn_cache_attend")
+    rc = load().lite_attn_cache_attend(plan, args, stream if stream.__class__ is int else _stream_ptr(stream))
+    if rc:
+        raise LiteAttnError(rc, "lite_attn_cache_attend")
 
 
 def lite_attn_prompt(plan: int, args, stream=None):
     """args: a PromptArgs' address, or its bytes."""
-    _check(load().lite_attn_prompt(plan, args, _stream_ptr(stream)), "lite_attn_prompt")
+    rc = load().lite_attn_prompt(plan, args, stream if stream.__class__ is int else _stream_ptr(stream))
+    if rc:
+        raise LiteAttnError(rc, "lite_attn_prompt")
 
 
 def lite_attn_launch_count() -> int:

@@ -174,13 +174,6 @@ class PagedCache:
             raise ValueError("a page must hold a power of two of tokens, 16 or more")
         return k_pages.data_ptr(), v_pages.data_ptr(), self.pages
 
-    def _pages(self):
-        """The pages where they are now: the tensors are the caller's, who may give them other memory."""
-        pool = self._pool
-        if self.k_pages.data_ptr() != pool[0] or self.v_pages.data_ptr() != pool[1]:
-            pool = self._pool = self._check_pages()
-        return pool
-
     def append(self, k, v, lens, cu_new, table, q=None, q_out=None, cos=None, sin=None, positions=None,
                interleaved: bool = False, stream=None):
         """New tokens' k and v ([tokens, Hk, d]) into the cache; q ([tokens, Hq, d]) into q_out.
@@ -208,7 +201,10 @@ class PagedCache:
             if rot % 16 or not 16 <= rot <= p.d:
                 raise ValueError("rot must be a multiple of 16, at most d")
             a = (cos.data_ptr(), sin.data_ptr(), rows)
-        B, width, pool = cu_new.numel() - 1, table.shape[-1], self._pages()
+        pool = self._pool      # the pages where they are now: the caller may have given the tensors other memory
+        if self.k_pages.data_ptr() != pool[0] or self.v_pages.data_ptr() != pool[1]:
+            pool = self._pool = self._check_pages()
+        B, width = cu_new.numel() - 1, table.shape[-1]
         args = _APPEND.pack(*rq, *ro, *rk, *rv, *pool, *a,
                             p._ints(positions, rk[1], "positions") if positions is not None else 0,
                             p._ints(cu_new, B + 1, "cu_new"), p._ints(lens, B, "lens"),
@@ -224,7 +220,10 @@ class PagedCache:
         host; it selects the kernel.  causal=False: every new token sees all keys of its
         sequence."""
         p = self.plan
-        rq, ro, pool = p._rows(q, p.Hq, "q"), p._rows(o, p.Hq, "o"), self._pages()
+        rq, ro = p._rows(q, p.Hq, "q"), p._rows(o, p.Hq, "o")
+        pool = self._pool      # as in append
+        if self.k_pages.data_ptr() != pool[0] or self.v_pages.data_ptr() != pool[1]:
+            pool = self._pool = self._check_pages()
         B, width = cu_new.numel() - 1, table.shape[-1]
         if max_new > rq[1]:
             max_new = rq[1]
