@@ -344,3 +344,78 @@ def test_pages_that_get_other_memory(way):
         cache.append(k, v, lens, cu, _ints(2).view(1, 1))
     with pytest.raises(ValueError):
         cache.attend(q, o[0], lens, cu, _ints(2).view(1, 1), max_new=T)
+
+
+def _first_calls_child():
+    """The library's first serving calls in the process are captured, and run when the graph is replayed."""
+    from temporal_block_sparse_sm_b200 import serving
+    Hq, Hk, d, T, page = 8, 2, 128, 70, 16
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    q, k, v = (_randn(T, h, d, seed=h + i) for i, h in enumerate((Hq, Hk, Hk)))
+    cache = serving.PagedCache(plan, *(torch.zeros(200, Hk, page, d, dtype=BF16, device="cuda") for _ in range(2)))
+    lens, cu, one = _ints(T), offsets([T]), offsets([1])
+    table = torch.arange(199, -1, -1, dtype=torch.int32, device="cuda").view(1, 200)
+    outs = [torch.full_like(q, 7.0) for _ in range(2)] + [torch.full_like(q[:1], 7.0)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        plan.prompt(q, k, v, outs[0], cu)
+        cache.append(k, v, lens, cu, table)
+        cache.attend(q, outs[1], lens, cu, table, max_new=T)
+        cache.attend(q[-1:], outs[2], lens, one, table, max_new=1)
+    graph.replay()
+    plan.check()
+    want, tol = seq_reference(q, k, v, True, d ** -0.5)
+    for o, rows in zip(outs, (slice(0, T), slice(0, T), slice(T - 1, T))):
+        assert_close(o, want[rows], tol[rows])
+    print("ok")
+
+
+def test_the_first_calls_of_a_process_are_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = "from tests.test_gpu_serving_callers import _first_calls_child; _first_calls_child()"
+    r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, PYTHONPATH=root), cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("stream_of", ["argument", "current"])
+def test_calls_on_a_forked_stream_of_a_capture(stream_of):
+    """A capture that forks to a second stream and joins it again, both with calls that need a workspace: the
+    graph's replays are right while other work takes the allocator's free memory."""
+    from temporal_block_sparse_sm_b200 import serving
+    Hq, Hk, d, page, m = 4, 1, 64, 64, 20000
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    cache = serving.PagedCache(plan, _randn(320, Hk, page, d), _randn(320, Hk, page, d, seed=1))
+    table, lens = torch.arange(320, dtype=torch.int32, device="cuda").view(1, 320), _ints(m)
+    qs = [_randn(n, Hq, d, seed=n) for n in (1, 60)]
+    outs, cus = [torch.empty_like(q) for q in qs], [offsets([q.shape[0]]) for q in qs]
+    call = lambda i, s=None: cache.attend(qs[i], outs[i], lens, cus[i], table, max_new=qs[i].shape[0], stream=s)   # noqa: E731
+    call(0), call(1)
+    plan.check()
+    want = [o.clone() for o in outs]
+    main, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        if stream_of == "argument":
+            call(0, side)
+        else:
+            with torch.cuda.stream(side):
+                call(0)
+        call(1)
+        main.wait_stream(side)
+    for _ in range(5):
+        for o in outs:
+            o.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 10, 1 << 16, 1 << 20, 1 << 23)]
+        with torch.cuda.stream(side):
+            junk += [torch.full((n,), float("nan"), device="cuda") for n in (1 << 10, 1 << 16, 1 << 20, 1 << 23)]
+        torch.cuda.synchronize()
+        del junk
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    plan.check()

@@ -83,7 +83,7 @@ def test_weights_far_below_the_largest_count_as_what_they_are(dtype, far, d, gap
 
 @pytest.mark.parametrize("dtype", [FP16, BF16])
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
-@pytest.mark.parametrize("new", [1, 4])
+@pytest.mark.parametrize("new", [1, 4, 40])
 @pytest.mark.parametrize("gap", [0, 3, 30])
 def test_values_that_are_not_finite_and_seen_by_all(dtype, value, new, gap):
     """An infinite value seen by every row, in the middle of a long cache and at its end, under a weight that
@@ -120,3 +120,20 @@ def test_logits_so_large_that_a_key_or_two_take_all(dtype, new, size, where):
     u = torch.finfo(dtype).eps / 2
     tol = (2 * u / (1 - u) + 2.0 ** -18) * torch.stack([v[where, 0].double().abs(), (v[where, 0].double().abs() + v[100, 0].double().abs()) / 2]) + u * want.abs()
     assert_close(o, want.expand(new, 2, d), (tol + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps).expand(new, 2, d))
+
+
+@pytest.mark.parametrize("dtype,d", [(FP16, 128), (BF16, 64)])
+@pytest.mark.parametrize("new", [3, 50])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(dtype, d, new):
+    g = _gen(6)
+    k, v = (torch.randn(400, 2, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn(new, 4, d, generator=g, device="cuda").to(dtype)
+    q[1, 2, 5], q[2, 0, 0], q[0, 3, 1] = math.nan, math.inf, -math.inf
+    o, refs = _attend(q, [k], [v], [new])
+    clean = q.clone()
+    clean[1, 2, 5], clean[2, 0, 0], clean[0, 3, 1] = 0, 0, 0
+    want, tol = seq_reference(clean, k, v, True, d ** -0.5)
+    spoilt = torch.zeros(new, 4, dtype=torch.bool, device="cuda")
+    spoilt[1, 2], spoilt[2, 0], spoilt[0, 3] = True, True, True
+    assert bool(torch.isnan(o[spoilt]).all())
+    assert_close(o[~spoilt], want[~spoilt], tol[~spoilt])
