@@ -419,3 +419,68 @@ def test_calls_on_a_forked_stream_of_a_capture(stream_of):
         del junk
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
     plan.check()
+
+
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_packed_rows_far_into_large_tensors(heads_first):
+    """q, k, v and o of over 2^31 elements each, the sequences in their last rows: offsets beyond 32 bits, in both
+    kernels, in the rotation, and where a value that is not finite is looked up again."""
+    import math
+
+    from temporal_block_sparse_sm_b200 import serving
+    Hq, Hk, d, n, m = 2, 1, 128, 60, 300
+    T = (1 << 31) // d + 1000                   # tokens of one head
+    def big(heads):
+        shape = (heads, T // heads, d) if heads_first else (T // heads, heads, d)
+        x = torch.empty(shape, dtype=BF16, device="cuda")
+        return x.transpose(0, 1) if heads_first else x
+    q, o, k, v = big(Hq), big(Hq), big(Hk), big(Hk)
+    tq, tk = q.shape[0], k.shape[0]
+    q[-n:], k[-m:], v[-m:] = _randn(n, Hq, d), _randn(m, Hk, d, seed=1), _randn(m, Hk, d, seed=2)
+    o[-n - 1:] = 7
+    v[-10, 0, 3] = math.inf                     # seen by the last rows only
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    cu_q, cu_k = torch.tensor([tq - n, tq], dtype=torch.int32, device="cuda"), torch.tensor([tk - m, tk], dtype=torch.int32, device="cuda")
+    plan.prompt(q, k, v, o, cu_q, cu_k)
+    plan.check()
+    want, tol = seq_reference(q[-n:], k[-m:], v[-m:], True, d ** -0.5)
+    assert_close(o[-n:], want, tol)
+    assert bool((o[-n - 1] == 7).all())
+    # the same rows into a cache, turned by nothing, and attended over by few rows and by many
+    pools = [torch.zeros(5, Hk, 64, d, dtype=BF16, device="cuda") for _ in range(2)]
+    cache, table = serving.PagedCache(plan, *pools), _ints(4, 2, 0, 1, 3).view(1, 5)
+    kq = big(Hq)                                # queries beside the new keys: as many rows
+    cu = torch.tensor([tq - m, tq], dtype=torch.int32, device="cuda")
+    kq[-m:] = _randn(m, Hq, d, seed=3)
+    o[-m:] = 7
+    cos, sin = serving.rotation_table([0] * m, [1.0] * (d // 2), device="cuda")
+    cache.append(k[tk - tq:], v[tk - tq:], _ints(m), cu, table, q=kq, q_out=o, cos=cos, sin=sin)
+    plan.check()
+    assert torch.equal(o[-m:], kq[-m:])
+    for rows in (2, n):
+        o[-n:] = 7
+        cache.attend(q, o, _ints(m), torch.tensor([tq - rows, tq], dtype=torch.int32, device="cuda"), table, max_new=rows)
+        plan.check()
+        assert_close(o[-rows:], want[-rows:], tol[-rows:])
+        assert bool((o[-n:-rows] == 7).all() if rows < n else True)
+
+
+@pytest.mark.parametrize("Hq,Hk,B", [(4, 4, 20000), (8, 1, 5000)])
+def test_a_large_batch_of_short_sequences(Hq, Hk, B):
+    """Thousands of sequences of one new token, keys by the dozen: every result against 64 bits at once."""
+    from temporal_block_sparse_sm_b200 import serving
+    d, page, m = 64, 16, 16
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    kp, vp, q = _randn(B, Hk, page, d), _randn(B, Hk, page, d, seed=1), _randn(B, Hq, d, seed=2)
+    lens = torch.arange(B, device="cuda").remainder(m + 1).int()
+    o = torch.full_like(q, 7.0)
+    serving.PagedCache(plan, kp, vp).attend(q, o, lens, torch.arange(B + 1, device="cuda").int(),
+                                            torch.arange(B, device="cuda").int().view(B, 1), max_new=1)
+    plan.check()
+    s = torch.einsum("bhgd,bhkd->bhgk", q.view(B, Hk, Hq // Hk, d).double(), kp.double()) / 8
+    hide = torch.arange(m, device="cuda")[None, :] >= lens[:, None]
+    w = torch.softmax(s.masked_fill(hide[:, None, None], float("-inf")), -1).nan_to_num(0.0)
+    want, A = (torch.einsum("bhgk,bhkd->bhgd", w, x).reshape(B, Hq, d) for x in (vp.double(), vp.double().abs()))
+    # u for the output, 2 u A for the weights; logits of up to 64 products of a few units each: 1e-4 is plenty for those
+    u = 2.0 ** -8
+    assert_close(o, want, u * want.abs() + (2 * u / (1 - u) + 1e-4) * A + 1e-30)
