@@ -18,9 +18,10 @@
 // an item's end, while the ring already fills with the next item's keys.
 //
 // Measured (B200, bf16, D = 128, in a graph): 64 single tokens of 32 heads over 277,485 cached
-// tokens of 8 key heads, 1138 MB, 186 us (6110 GB/s, 0.93 of a plain copy); one token over 1,000
-// 12.1 us, of which walking to the first load and the join after the last part take 3 us each.  Q K^T
-// in two accumulators was slower.
+// tokens of 8 key heads, 1138 MB, 185 us (6140 GB/s, 0.94 of a plain copy); one token over 1,000
+// 12.6 us, of which walking to the first load and the join after the last part take 3 us each.  Q K^T
+// in two accumulators was slower.  Up to three of two blocks' ten warps share a quarter of the SM's
+// registers, 168 a thread; at D = 128 that is 20 (bf16) and 32 bytes (fp16) short, which are spilled.
 //
 // Values that no row sees (behind the last key, in a page's unused part) are zeroed in
 // shared memory before the product, since 0 * NaN is NaN.  Where some rows see a key that

@@ -201,10 +201,11 @@ struct Division {
 // over 8,000 keys 23.7 -> 25.7 us (300 over 2,300: 28.0 -> 27.0).
 constexpr int kTileItemCost = 256, kTileJoinCost = 1280, kTileMinStretch = 256;
 constexpr int kRowsItemCost = 96, kRowsJoinCost = 320, kRowsMinStretch = 128;
-// Eighths of a key that a key costs an item whose second slot is empty, measured: 6 at d = 128 (a
-// 1,560-token frame over 32,760 keys of 12 heads, 6.1 items a head: 378 us with 8, 361 with 6, 414
-// with 4), all 8 at d = 64 (880 tokens over 14,000 keys of 24 heads: 141 us with 8 or 6, 160 with
-// 5; 11 chunks of up to 513 tokens: 164 us with 8, 170 with 6).
+// Eighths of a key that a key costs an item whose second slot is empty, measured with 4, 5, 6 and 8 in turn, not
+// causal.  At d = 128, 1,560 tokens over 32,760 keys of 12 heads: 412, 344, 329 and 341 us; 880 over 14,000 of 24:
+// 213, 197, 193, 196; 1,100 over 20,000 of 16: 268, 230, 233, 235; 2,080 over 16,640, 24 heads on 8: 400 to 407; but
+// 300 over 9,000 of 8: 41, 44, 49, 46.  At d = 64 the same five: 385, 315, 273, 272; 187, 160, 145, 148; (1,100 not
+// measured); 309 all; 35, 35, 35, 37; and 11 causal chunks of up to 513 tokens over up to 16,514: 206, 174, 151, 146.
 constexpr int kTileHalfWeight128 = 6, kTileHalfWeight64 = 8;
 constexpr int kManyItems = 8;   // items per block from which whole items come out even within an eighth: no workspace
 
@@ -222,9 +223,9 @@ Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_
         int64_t per = 2 * (128 / G);
         dv.rows = 256;
         dv.items = pl->Hk * std::min((tokens + B * (per - 1)) / per, tokens);
-        // A slot by itself takes two thirds of the time of two side by side: where there are blocks for all
-        // slots of a batch, and no item is cut, an item is one of them (64 tokens over 1000 keys, 16 heads
-        // over 4: 17.9 instead of 23.1 us; a prompt of 500, 32 heads over 8: 14.2 instead of 16.9; of 200: the same).
+        // Where there are blocks for all slots of a batch, and no item is cut, an item is one slot: alone it ends
+        // before two side by side would (64 tokens over 1000 keys, 16 heads over 4: 17.9 instead of 23.1 us; a
+        // prompt of 500, 32 heads over 8: 14.2 instead of 16.9; of 200: the same).
         const int64_t singles = pl->Hk * std::min((tokens + B * (per / 2 - 1)) / (per / 2), tokens);
         if (singles <= pl->sms && max_keys <= kTileJoinCost) {
             dv.slots = 1;
@@ -243,10 +244,11 @@ Division divide(const lite_attn_gqa *pl, int64_t B, int64_t tokens, int64_t max_
     dv.split = least < kManyItems * most && max_keys > (dv.tile ? kTileJoinCost : kRowsJoinCost);
     // no more blocks than there can be items, unless items may be cut
     dv.blocks = dv.split ? most : static_cast<int>(std::min<int64_t>(dv.items, most));
-    // By a counter, where several sequences have more items than there are blocks: 16 prompts of 1 to 2048
-    // tokens 290 -> 262 us, 5 uneven ones 277 -> 254; of equal sequences it costs the counter's memset and an end
-    // less even: 40 chunks of 100 over 600 keys 72.6 -> 75.8, 30 of 300 over 1,200 102 -> 109 us.  One
-    // sequence's items fall off in length evenly: nothing to gain there.
+    // By a counter, where several sequences have more items than there are blocks, against back and forth: 16
+    // prompts of 1 to 2,048 tokens 276 -> 236 and 282 -> 256 us (two draws), 12 of 500 to 4,000 525 -> 512, 5 uneven
+    // ones at d = 64 277 -> 260, 6 of 4,096 each 819 -> 781, 30 chunks of 300 over 1,200 keys 186 -> 177; it can cost the
+    // counter's memset: 40 chunks of 100 over 600 keys 75.4 -> 76.5.  One sequence's items fall off in length evenly:
+    // nothing to gain there.
     dv.by_counter = !dv.split && B > 1 && least > most;
     dv.workspace = dv.split ? static_cast<size_t>(dv.blocks) * (2 * static_cast<size_t>(dv.rows) * (pl->d + 2) * 4u + sizeof(JoinItem))
                             : dv.by_counter ? sizeof(int) : 0;

@@ -13,7 +13,8 @@
 // Division among the blocks.  A batch of many items (block of query rows, key head) is dealt
 // out whole, in order of length within a sequence: of one sequence back and forth over the blocks,
 // of several by a counter, to whichever block asks next (an item's result does not depend on its
-// block; back and forth, the longest block of a ragged batch had a quarter more than the mean).  With few
+// block; back and forth, counting keys, the longest block of 16 prompts of 1 to 2,048 tokens would get a
+// quarter more than the mean).  With few
 // items the batch is laid out on a line instead, an item taking as many units as its last row
 // sees keys (half_weight eighths of that where it fills only the first of the tile kernel's two
 // slots), and item_cost for its start and end; each block takes an equal stretch of the line,
