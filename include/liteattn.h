@@ -365,7 +365,8 @@ int lite_attn_compact_noalloc(const uint32_t *bits, int B, int H, int N, int Br,
  * - A grouped-query plan fixes Hq query heads, Hk key heads (query head h reads
  *   key head h / (Hq / Hk)), d and the 16-bit type of all tensors.  It belongs
  *   to the device that was current when it was created.  It holds no scratch:
- *   calls with different workspaces may overlap on different streams.
+ *   calls with different workspaces may overlap on different streams.  It must
+ *   live as long as graphs that captured its calls are replayed.
  * - Tensors are [tokens][heads][d] views (lite_attn_rows_t): d contiguous, token
  *   and head strides multiples of 8 elements, 16-byte aligned, so slices of a
  *   fused projection serve as they are.

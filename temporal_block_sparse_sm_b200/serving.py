@@ -46,7 +46,8 @@ class GroupedPlan:
     """Hq query heads in groups over Hk key heads, head dim d (64 or 128), bf16 or fp16.
 
     The plan belongs to the device that is current when it is made.  It holds no
-    scratch, so its calls may run on several streams at once."""
+    scratch, so its calls may run on several streams at once.  Keep it as long as
+    graphs that captured its calls are replayed."""
 
     def __init__(self, Hq: int, Hk: int, d: int, dtype=None):
         import torch
