@@ -386,6 +386,11 @@ struct BlockWalk {
     }
 };
 
+namespace ptx {
+// Orders this thread's ordinary accesses to shared memory before later ones of the async proxy (TMA, MMA operands).
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+}  // namespace ptx
+
 // All kernels here are launched so that they may start before the kernel in front of them on the
 // stream has ended (and set up what touches no memory).  Every thread waits for that one, and for
 // its writes, before its own first access, whatever its block has to do, so that a kernel's end
