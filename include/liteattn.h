@@ -460,8 +460,8 @@ typedef struct {
 int lite_attn_cache_append(lite_attn_gqa_t plan, const lite_attn_append_t *args, void *stream);
 
 /* Attention of new tokens over the cache.
- *   q, o     : [tokens][Hq][d] views; o must not overlap q, the cache or the
- *              workspace.
+ *   q, o     : [tokens][Hq][d] views; o must not overlap anything else of the
+ *              call (nor must q_out and the pages above).
  *   lens     : device [B], keys of each sequence (the new tokens' own included,
  *              appended before).  Cache, cu_new and table as above.
  *   max_new  : an upper bound of the new tokens of a sequence, known to the

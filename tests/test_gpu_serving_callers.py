@@ -484,3 +484,27 @@ def test_a_large_batch_of_short_sequences(Hq, Hk, B):
     # u for the output, 2 u A for the weights; logits of up to 64 products of a few units each: 1e-4 is plenty for those
     u = 2.0 ** -8
     assert_close(o, want, u * want.abs() + (2 * u / (1 - u) + 1e-4) * A + 1e-30)
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_pages_that_sequences_share(new):
+    """Sequences with a common beginning hold it once; a page may even come twice in one sequence; and keys may
+    be values (one tensor for both)."""
+    from temporal_block_sparse_sm_b200 import serving
+    Hq, Hk, d, page, m = 4, 2, 64, 16, 90
+    kp, vp = _randn(12, Hk, page, d), _randn(12, Hk, page, d, seed=1)
+    table = _ints([3, 7, 1, 0, 5, 2], [3, 7, 1, 4, 6, 8], [3, 3, 3, 3, 9, 3])
+    plan = serving.GroupedPlan(Hq, Hk, d)
+    q = _randn(3 * new, Hq, d, seed=2)
+    o = torch.empty_like(q)
+    serving.PagedCache(plan, kp, vp).attend(q, o, _ints(m, m, m), offsets([new] * 3), table, max_new=new)
+    plan.check()
+    for b in range(3):
+        k, v = (torch.cat([p[int(j)].transpose(0, 1) for j in table[b]])[:m] for p in (kp, vp))
+        rows = slice(b * new, (b + 1) * new)
+        want, tol = seq_reference(q[rows], k, v, True, d ** -0.5)
+        assert_close(o[rows], want, tol, f"sequence {b}")
+    plan.prompt(q, k, k, o, offsets([3 * new]), offsets([m]))
+    plan.check()
+    want, tol = seq_reference(q, k, k, True, d ** -0.5)
+    assert_close(o, want, tol)
